@@ -1,4 +1,5 @@
-"""MI355X (gfx950) DoRA hot path: factored row norm and fused compose.
+"""MI355X (gfx950) DoRA hot path: factored row norm and fused compose, and the
+8-bit operators around a weight held in 8 bits.
 
 The computation lives in the HIP library libdora_mi355x.so (C ABI declared in
 include/dora.h); this package holds its sources (csrc/), the build step and a
@@ -25,4 +26,18 @@ from .binding import (  # noqa: F401
     merge_workspace_size,
     norm_group_workspace_size,
     norm_workspace_size,
+)
+from .eightbit import (  # noqa: F401
+    LinearQ8,
+    RMSNorm,
+    dequantize_rows,
+    linear_q8,
+    linear_q8_backward,
+    matmul_q8,
+    matmul_q8_workspace_size,
+    quantize_rows,
+    rmsnorm,
+    rmsnorm_backward,
+    rmsnorm_backward_workspace_size,
+    rmsnorm_q8,
 )

@@ -57,6 +57,15 @@ _SIGNATURES = {
                                          _vp]),
     "dora_compose_backward_inner": (ctypes.c_int, [_vp, _vp, _vp, _vp, _f32, _f32, _i64, _i64, ctypes.c_int,
                                                    ctypes.c_int, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dora_rmsnorm": (ctypes.c_int, [_vp, _vp, _vp, _f32, _i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "dora_rmsnorm_backward_workspace_size": (ctypes.c_int, [_i64, _i64, ctypes.POINTER(_sz)]),
+    "dora_rmsnorm_backward": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, ctypes.c_int, _vp, _vp, _vp, _sz,
+                                             _vp]),
+    "dora_quantize_rows": (ctypes.c_int, [_vp, _vp, _i64, _i64, ctypes.c_int, _vp, _vp, _vp]),
+    "dora_dequantize_rows": (ctypes.c_int, [_vp, _vp, _i64, _i64, ctypes.c_int, _vp, _vp]),
+    "dora_matmul_q8_workspace_size": (ctypes.c_int, [_i64, _i64, _i64, ctypes.POINTER(_sz)]),
+    "dora_matmul_q8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _i64, _i64, _i64, ctypes.c_int, _vp,
+                                      _vp, _sz, _vp]),
 }
 EXPORTED = tuple(_SIGNATURES)
 

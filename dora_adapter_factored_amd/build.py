@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libdora_mi355x.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
-SOURCES = ("dora_capi.hip", "compose.hip", "norm.hip", "merge.hip")
+SOURCES = ("dora_capi.hip", "compose.hip", "norm.hip", "merge.hip", "rownorm.hip", "matmul_q8.hip")
 # measurement-only kernels (bench.py --ceilings), a library of their own
 CEILINGS_LIB_PATH = os.path.join(PKG, "libdora_ceilings.so")
 CEILINGS_SOURCES = ("ceilings.hip",)

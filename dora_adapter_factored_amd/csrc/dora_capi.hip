@@ -103,7 +103,7 @@ const char* dora_status_string(int status) {
 
 const char* dora_last_error_detail(void) { return g_detail; }
 
-int dora_version(void) { return 200; }
+int dora_version(void) { return 300; }
 
 int dora_factored_norm_workspace_size(int64_t d_out, int64_t d_in, int64_t r, int dtype, size_t* bytes) {
     if (!bytes) return fail(DORA_ERR_INVALID_ARG, "bytes is NULL");
@@ -337,6 +337,125 @@ int dora_merge(const void* W0, const void* A, const void* B, const float* g, flo
     hipError_t e = dora::launch_merge(W0, A, B, g, s, d_out, d_in, r, dtype, W, workspace,
                                       static_cast<hipStream_t>(stream));
     return hip_status(e, "dora_merge launch");
+}
+
+namespace {
+
+int check_rows(int64_t n, int64_t d, int dtype) {
+    if (!dim_ok(d, 1) || !dim_ok(n, 0))
+        return fail(DORA_ERR_INVALID_ARG, "sizes must satisfy 1 <= row length < 2^31, 0 <= rows < 2^31 (got %lld rows of %lld)",
+                    (long long)n, (long long)d);
+    if (!dtype_ok(dtype)) return fail(DORA_ERR_INVALID_ARG, "unknown dtype code %d", dtype);
+    return DORA_OK;
+}
+
+int check_workspace(const void* workspace, size_t have, size_t need) {
+    if (need == 0) return DORA_OK;
+    if (!workspace) return fail(DORA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
+    if (have < need) return fail(DORA_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", have, need);
+    if (!aligned256(workspace)) return fail(DORA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+    return DORA_OK;
+}
+
+// int32 holds any sum of this many products of two bytes: 131071 * 2^14 < 2^31
+constexpr int64_t kMaxQ8Depth = 131071;
+
+int check_q8_sizes(int64_t T, int64_t d_out, int64_t d_in) {
+    if (!dim_ok(T, 0) || !dim_ok(d_out, 1) || !dim_ok(d_in, 1))
+        return fail(DORA_ERR_INVALID_ARG, "sizes must satisfy 0 <= T < 2^31, 1 <= d_out, d_in < 2^31 (got %lld, %lld, %lld)",
+                    (long long)T, (long long)d_out, (long long)d_in);
+    if (d_in > kMaxQ8Depth)
+        return fail(DORA_ERR_UNSUPPORTED, "d_in is %lld; an int32 sum holds at most %lld products", (long long)d_in,
+                    (long long)kMaxQ8Depth);
+    return DORA_OK;
+}
+
+}  // namespace
+
+int dora_rmsnorm(const void* x, const void* residual, const void* w, float eps, int64_t T, int64_t d, int dtype,
+                 void* h, void* y, int8_t* q, float* qscale, float* rstd, void* stream) {
+    const int st = check_rows(T, d, dtype);
+    if (st != DORA_OK) return st;
+    if (!w) return fail(DORA_ERR_INVALID_ARG, "w must be non-NULL");
+    if (T != 0 && !x) return fail(DORA_ERR_INVALID_ARG, "x must be non-NULL when T > 0");
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return fail(DORA_ERR_INVALID_ARG, "eps must be finite and > 0");
+    if (T != 0 && (q == nullptr) != (qscale == nullptr))
+        return fail(DORA_ERR_INVALID_ARG, "q and qscale are given together or not at all");
+    if (T != 0 && !h && !y && !q && !rstd) return fail(DORA_ERR_INVALID_ARG, "no output is given");
+    if (T != 0 && y && (y == x || y == residual || y == h)) return fail(DORA_ERR_INVALID_ARG, "y must not alias x, residual or h");
+    hipError_t e = dora::launch_rmsnorm(x, residual, w, eps, T, d, dtype, h, y, q, qscale, rstd,
+                                        static_cast<hipStream_t>(stream));
+    return hip_status(e, "dora_rmsnorm launch");
+}
+
+int dora_rmsnorm_backward_workspace_size(int64_t T, int64_t d, size_t* bytes) {
+    if (!bytes) return fail(DORA_ERR_INVALID_ARG, "bytes is NULL");
+    const int st = check_rows(T, d, DORA_F32);
+    if (st != DORA_OK) return st;
+    *bytes = dora::rmsnorm_bwd_workspace_bytes(T, d);
+    return ok();
+}
+
+int dora_rmsnorm_backward(const void* dy, const void* h, const void* w, const float* rstd, const void* dh, int64_t T,
+                          int64_t d, int dtype, void* dx, float* dw, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    int st = check_rows(T, d, dtype);
+    if (st != DORA_OK) return st;
+    if (!w) return fail(DORA_ERR_INVALID_ARG, "w must be non-NULL");
+    if (T != 0 && (!dy || !h || !rstd || !dx))
+        return fail(DORA_ERR_INVALID_ARG, "dy, h, rstd and dx must be non-NULL when T > 0");
+    if (T != 0 && dx == h) return fail(DORA_ERR_INVALID_ARG, "dx may alias dy or dh only");
+    if (dw) {
+        st = check_workspace(workspace, workspace_bytes, dora::rmsnorm_bwd_workspace_bytes(T, d));
+        if (st != DORA_OK) return st;
+    }
+    hipError_t e = dora::launch_rmsnorm_bwd(dy, h, w, rstd, dh, T, d, dtype, dx, dw, workspace,
+                                            static_cast<hipStream_t>(stream));
+    return hip_status(e, "dora_rmsnorm_backward launch");
+}
+
+int dora_quantize_rows(const void* x, const float* col_scale, int64_t n, int64_t d, int dtype, int8_t* q, float* scale,
+                       void* stream) {
+    const int st = check_rows(n, d, dtype);
+    if (st != DORA_OK) return st;
+    if (n != 0 && (!x || !q || !scale)) return fail(DORA_ERR_INVALID_ARG, "x, q and scale must be non-NULL when n > 0");
+    hipError_t e = dora::launch_quantize_rows(x, col_scale, n, d, dtype, q, scale, static_cast<hipStream_t>(stream));
+    return hip_status(e, "dora_quantize_rows launch");
+}
+
+int dora_dequantize_rows(const int8_t* q, const float* scale, int64_t n, int64_t d, int dtype, void* out, void* stream) {
+    const int st = check_rows(n, d, dtype);
+    if (st != DORA_OK) return st;
+    if (n != 0 && (!q || !scale || !out)) return fail(DORA_ERR_INVALID_ARG, "q, scale and out must be non-NULL when n > 0");
+    hipError_t e = dora::launch_dequantize_rows(q, scale, n, d, dtype, out, static_cast<hipStream_t>(stream));
+    return hip_status(e, "dora_dequantize_rows launch");
+}
+
+int dora_matmul_q8_workspace_size(int64_t T, int64_t d_out, int64_t d_in, size_t* bytes) {
+    if (!bytes) return fail(DORA_ERR_INVALID_ARG, "bytes is NULL");
+    const int st = check_q8_sizes(T, d_out, d_in);
+    if (st != DORA_OK) return st;
+    *bytes = dora::matmul_q8_workspace_bytes(T, d_out, d_in);
+    return ok();
+}
+
+int dora_matmul_q8(const int8_t* xq, const float* xscale, const int8_t* wq, const float* wscale, const float* bias,
+                   const float* g, const void* lora_out, float s, int64_t T, int64_t d_out, int64_t d_in, int dtype,
+                   void* y, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = check_q8_sizes(T, d_out, d_in);
+    if (st != DORA_OK) return st;
+    if (!dtype_ok(dtype)) return fail(DORA_ERR_INVALID_ARG, "unknown dtype code %d", dtype);
+    if (!wq) return fail(DORA_ERR_INVALID_ARG, "wq must be non-NULL");
+    if (T != 0 && (!xq || !xscale || !y)) return fail(DORA_ERR_INVALID_ARG, "xq, xscale and y must be non-NULL when T > 0");
+    if (T != 0 && (g == nullptr) != (lora_out == nullptr))
+        return fail(DORA_ERR_INVALID_ARG, "g and lora_out are given together or not at all");
+    if (!std::isfinite(s)) return fail(DORA_ERR_INVALID_ARG, "s must be finite");
+    if (T != 0 && (y == xq || y == wq)) return fail(DORA_ERR_INVALID_ARG, "y may alias lora_out only");
+    st = check_workspace(workspace, workspace_bytes, dora::matmul_q8_workspace_bytes(T, d_out, d_in));
+    if (st != DORA_OK) return st;
+    const dora::MatmulQ8 a{xq, xscale, wq, wscale, bias, g, lora_out, s, T, d_out, d_in, y};
+    hipError_t e = dora::launch_matmul_q8(a, dtype, workspace, static_cast<hipStream_t>(stream));
+    return hip_status(e, "dora_matmul_q8 launch");
 }
 
 }  // extern "C"

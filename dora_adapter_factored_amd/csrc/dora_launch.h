@@ -96,4 +96,43 @@ hipError_t launch_merge(const void* W0, const void* A, const void* B, const floa
                         int64_t d_out, int64_t d_in, int64_t r, int dtype, void* W, void* workspace,
                         hipStream_t stream);
 
+// ------------------------------------------------------------ row operators
+
+// Outputs h, y, q (with scale) and rstd may be nullptr; res may be nullptr.
+hipError_t launch_rmsnorm(const void* x, const void* res, const void* w, float eps, int64_t rows, int64_t d, int dtype,
+                          void* h, void* y, int8_t* q, float* scale, float* rstd, hipStream_t stream);
+
+size_t rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t d);
+
+// dh and dw may be nullptr; the workspace is used when dw is given.
+hipError_t launch_rmsnorm_bwd(const void* dy, const void* h, const void* w, const float* rstd, const void* dh,
+                              int64_t rows, int64_t d, int dtype, void* dx, float* dw, void* workspace,
+                              hipStream_t stream);
+
+hipError_t launch_quantize_rows(const void* x, const float* col_scale, int64_t rows, int64_t d, int dtype, int8_t* q,
+                                float* scale, hipStream_t stream);
+
+hipError_t launch_dequantize_rows(const int8_t* q, const float* scale, int64_t rows, int64_t d, int dtype, void* out,
+                                  hipStream_t stream);
+
+// ------------------------------------------------------------ 8-bit product
+
+// y [T, N] = composed (xq [T, K] scaled by xs [T]) (wq [N, K] scaled by ws [N])^T
+struct MatmulQ8 {
+    const int8_t* xq;
+    const float* xs;
+    const int8_t* wq;
+    const float* ws;     // or nullptr: ones
+    const float* bias;   // or nullptr
+    const float* g;      // or nullptr: no composition
+    const void* lora;
+    float s;
+    int64_t T, N, K;
+    void* y;
+};
+
+size_t matmul_q8_workspace_bytes(int64_t T, int64_t N, int64_t K);
+
+hipError_t launch_matmul_q8(const MatmulQ8& a, int dtype, void* workspace, hipStream_t stream);
+
 }  // namespace dora

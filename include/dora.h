@@ -1,6 +1,7 @@
 /*
  * dora.h -- C ABI of the MI355X (gfx950) DoRA hot path: factored row norm and
- * fused compose, forward and backward.
+ * fused compose, forward and backward; the merge for serving; and the 8-bit
+ * operators around a weight held in 8 bits.
  *
  * Sources, cited by short title and section:
  *   [ScalingDoRA]  "Scaling DoRA: High-Rank Adaptation via Factored Norms and
@@ -314,6 +315,125 @@ int dora_merge_workspace_size(int64_t d_in, int64_t r, int dtype, size_t* bytes)
 int dora_merge(const void* W0, const void* A, const void* B, const float* g, float s, int64_t d_out,
                int64_t d_in, int64_t r, int dtype, void* W, void* workspace, size_t workspace_bytes,
                void* stream);
+
+/*
+ * ------------------------------------------------------- 8-bit operators
+ *
+ * A weight held in 8 bits is a matrix of signed codes in [-127, 127] with one
+ * fp32 scale per row (output channel); an activation in 8 bits is the same
+ * with one scale per token.  A code stands for code * scale.  Rounding is to
+ * nearest even and symmetric: scale = (largest |value| of the row) / 127.
+ *   - A row of zeros has scale 0 and codes 0; so has one whose largest |value|
+ *     is below 2^-119.
+ *   - A row that holds a NaN or an infinity has scale NaN and codes 0, so that
+ *     everything computed from it is NaN.
+ */
+
+/*
+ * Root-mean-square norm of x plus the residual, one pass:
+ *   h    = x + residual                      (h = x when residual is NULL)
+ *   rstd = 1 / sqrt(mean_j h_j^2 + eps)      per row
+ *   y    = h * rstd * w
+ *   q, qscale = y in 8 bits (before y is rounded to dtype)
+ * in fp32, each output rounded once (round-to-nearest-even) to its type; the
+ * norm is that of h before h is rounded.
+ *
+ *   x, residual   device [T, d], dtype; residual may be NULL.
+ *   w             device [d], dtype.
+ *   eps           > 0.
+ *   h             device [T, d], dtype, output; may be NULL; may alias x or
+ *                 residual exactly (in place).
+ *   y             device [T, d], dtype, output, or NULL.
+ *   q, qscale     device int8 [T, d] and fp32 [T], outputs, both or neither.
+ *   rstd          device fp32 [T], output, or NULL; dora_rmsnorm_backward
+ *                 takes it.
+ * At least one output is given.  Outputs must not overlap each other or, but
+ * for h, an input.  T == 0 is a no-op; T < 2^31.
+ */
+int dora_rmsnorm(const void* x, const void* residual, const void* w, float eps, int64_t T, int64_t d, int dtype,
+                 void* h, void* y, int8_t* q, float* qscale, float* rstd, void* stream);
+
+/* Workspace bytes needed by dora_rmsnorm_backward when dw != NULL. */
+int dora_rmsnorm_backward_workspace_size(int64_t T, int64_t d, size_t* bytes);
+
+/*
+ * Backward of dora_rmsnorm's y and h:
+ *   u    = w * dy
+ *   dx   = rstd * (u - h * rstd^2 * mean_j(u_j h_j)) + dh
+ *   dw_j = sum_t dy_tj h_tj rstd_t
+ * dx is the gradient of x and of the residual alike.  dw is summed in a fixed
+ * order, so results are bitwise reproducible.
+ *
+ *   dy, h         device [T, d], dtype; h as dora_rmsnorm wrote it (x where
+ *                 there was no residual).
+ *   w             device [d], dtype.
+ *   rstd          device fp32 [T].
+ *   dh            device [T, d], dtype: the gradient that reaches h by its
+ *                 other uses, or NULL.
+ *   dx            device [T, d], dtype, output; may alias dy or dh exactly.
+ *   dw            device fp32 [d], output (overwritten), or NULL when w is
+ *                 frozen.
+ *   workspace     needed only when dw != NULL: at least
+ *                 dora_rmsnorm_backward_workspace_size() bytes, 256-byte
+ *                 aligned, no initialisation needed.
+ * T == 0 writes zeros to dw and nothing else.
+ */
+int dora_rmsnorm_backward(const void* dy, const void* h, const void* w, const float* rstd, const void* dh, int64_t T,
+                          int64_t d, int dtype, void* dx, float* dw, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/*
+ * The rows of x * col_scale in 8 bits: a weight [d_out, d_in] when it is
+ * loaded (W of dora_merge, or W0), an activation before a product, or an
+ * output gradient scaled by a weight's channel scales before the product that
+ * gives the input's gradient.
+ *
+ *   x             device [n, d], dtype.
+ *   col_scale     device fp32 [d], or NULL for ones.
+ *   q, scale      device int8 [n, d] and fp32 [n], outputs.
+ * n == 0 is a no-op; n < 2^31.
+ */
+int dora_quantize_rows(const void* x, const float* col_scale, int64_t n, int64_t d, int dtype, int8_t* q, float* scale,
+                       void* stream);
+
+/*
+ * out = q * scale by rows, rounded once to dtype: for operators that take the
+ * weight itself, such as dora_factored_norm.
+ */
+int dora_dequantize_rows(const int8_t* q, const float* scale, int64_t n, int64_t d, int dtype, void* out, void* stream);
+
+/*
+ * Product of an activation and a weight in 8 bits, with the DoRA composition
+ * and a bias in the same call:
+ *   base_tn = xscale_t * wscale_n * sum_k xq_tk wq_nk
+ *   y_tn    = base_tn + ((g_n - 1) base_tn + (g_n s) lora_tn) + bias_n
+ * The sum is exact (int32); what follows is fp32, rounded once
+ * (round-to-nearest-even) to dtype.  base is never rounded or written.
+ *
+ *   xq, xscale    device int8 [T, d_in], fp32 [T].
+ *   wq            device int8 [d_out, d_in] (nn.Linear layout).
+ *   wscale        device fp32 [d_out], or NULL for ones: with the transposed
+ *                 codes [d_in, d_out] and an activation that
+ *                 dora_quantize_rows scaled by wscale, the call is the
+ *                 product of the input's gradient.
+ *   bias          device fp32 [d_out], or NULL.
+ *   g, lora_out   device fp32 [d_out] and [T, d_out] of dtype (excludes s), or
+ *                 both NULL: no composition.
+ *   y             device [T, d_out], dtype, output; may alias lora_out
+ *                 exactly.
+ *   d_in          at most 131071, which no int32 sum of products can leave.
+ * T == 0 is a no-op; T < 2^31.
+ */
+int dora_matmul_q8(const int8_t* xq, const float* xscale, const int8_t* wq, const float* wscale, const float* bias,
+                   const float* g, const void* lora_out, float s, int64_t T, int64_t d_out, int64_t d_in, int dtype,
+                   void* y, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Workspace bytes needed by dora_matmul_q8 for these sizes (host call,
+ * launches nothing); 0 is possible.  The workspace is 256-byte aligned and
+ * needs no initialisation.
+ */
+int dora_matmul_q8_workspace_size(int64_t T, int64_t d_out, int64_t d_in, size_t* bytes);
 
 #ifdef __cplusplus
 }
