@@ -29,13 +29,25 @@ __device__ __forceinline__ i32x4_t load16(const int8_t* p) {
     return v;
 }
 
-// The first `left` of 16 bytes, zeros after them.
-__device__ __forceinline__ i32x4_t load16_tail(const int8_t* p, int64_t left) {
-    if (left >= 16) return load16(p);
+// Bytes k .. k + 15 of a row of K, zeros past its end: the last 16 bytes of
+// the row moved down, so that nothing outside the row is read.
+__device__ __forceinline__ i32x4_t load16_tail(const int8_t* row, int k, int K) {
     i32x4_t v = {0, 0, 0, 0};
-#pragma unroll
-    for (int b = 0; b < 16; ++b)
-        if (b < left) v[b / 4] |= (int)(uint8_t)p[b] << (8 * (b % 4));
+    if (K < 16) {
+        for (int b = 0; b < 16; ++b)
+            if (k + b < K) v[b / 4] |= (int)(uint8_t)row[k + b] << (8 * (b % 4));
+        return v;
+    }
+    const int at = k < K - 16 ? k : K - 16, skip = 8 * (k - at);   // bits
+    const i32x4_t r = load16(row + at);
+    uint64_t lo = (uint32_t)r[0] | (uint64_t)(uint32_t)r[1] << 32, hi = (uint32_t)r[2] | (uint64_t)(uint32_t)r[3] << 32;
+    if (skip >= 128) lo = hi = 0;
+    else if (skip >= 64) lo = hi >> (skip - 64), hi = 0;
+    else if (skip > 0) lo = lo >> skip | hi << (64 - skip), hi >>= skip;
+    v[0] = (int)(uint32_t)lo;
+    v[1] = (int)(uint32_t)(lo >> 32);
+    v[2] = (int)(uint32_t)hi;
+    v[3] = (int)(uint32_t)(hi >> 32);
     return v;
 }
 
@@ -91,33 +103,35 @@ __global__ __launch_bounds__(kWaves * 64) void q8_direct(MatmulQ8 a) {
     // rows past the end repeat the last one; their results are not stored
     const int64_t nr = n0 + (lane & 15) < a.N ? n0 + (lane & 15) : a.N - 1;
     const int kl = (lane >> 4) * 32;
-    const int8_t* wp = a.wq + nr * a.K + kl;
+    const int K = (int)a.K;
+    const int8_t* wp = a.wq + nr * K;
     const int8_t* xp[C];
     i32x4_t acc[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int64_t t = t0 + c * 16 + (lane & 15);
-        xp[c] = a.xq + (t < a.T ? t : a.T - 1) * a.K + kl;
+        xp[c] = a.xq + (t < a.T ? t : a.T - 1) * K;
         acc[c] = {0, 0, 0, 0};
     }
-    const int64_t full = a.K / 128;
-    for (int64_t kb = wave; kb < full; kb += kWaves) {
+    const int full = K / 128;
+    for (int kb = wave; kb < full; kb += kWaves) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const i32x4_t w = load16(wp + kb * 128 + j * 16);
+            const int k = kb * 128 + kl + j * 16;
+            const i32x4_t w = load16(wp + k);
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, load16(xp[c] + kb * 128 + j * 16), acc[c], 0, 0, 0);
+                acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, load16(xp[c] + k), acc[c], 0, 0, 0);
         }
     }
-    if (full % kWaves == wave && full * 128 < a.K) {
+    if (full % kWaves == wave && full * 128 < K) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const int64_t k = full * 128 + j * 16, left = a.K - k - kl;
-            const i32x4_t w = load16_tail(wp + k, left);
+            const int k = full * 128 + kl + j * 16;
+            const i32x4_t w = load16_tail(wp, k, K);
 #pragma unroll
             for (int c = 0; c < C; ++c)
-                acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, load16_tail(xp[c] + k, left), acc[c], 0, 0, 0);
+                acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, load16_tail(xp[c], k, K), acc[c], 0, 0, 0);
         }
     }
 #pragma unroll
@@ -141,85 +155,106 @@ __global__ __launch_bounds__(kWaves * 64) void q8_direct(MatmulQ8 a) {
 
 // ------------------------------------------------------------- tiles through LDS
 
+constexpr int kNumCU = 256;
 constexpr int kNumXCD = 8;
 
-// BM tokens x BN channels per workgroup, k-tiles of 128 codes (whole 128-byte
-// rows) of both operands in a two-stage LDS ring, filled by LDS DMA.
+// BM tokens x BN channels per workgroup of 8 waves, k-tiles of 128 codes
+// (whole 128-byte rows) of both operands in an LDS ring of S stages.
 //
-// Rows of an LDS tile keep their order; a 16-row MFMA block b of a 64-row
-// group takes rows 16 (r / 4) + 4 b + r % 4, r = 0..15.  Lane l's results of
-// the group's four channel blocks are then the 16 consecutive channels 16 (l /
-// 16) + 0..15 of one token, so that results go from registers to memory in
-// runs of 64 channels per token, without a pass through LDS.
+// Rows of an LDS tile keep their order.  Of a 64-channel group, the 16-row
+// MFMA block b takes rows 16 (r / 4) + 4 b + r % 4, r = 0..15: lane l's
+// results of the group's four blocks are then the 16 consecutive channels
+// 16 (l / 16) + 0..15 of one token, and results go from registers to memory in
+// runs of 64 channels per token, without a pass through LDS.  Token blocks
+// take 16 rows in order.
 //
-// Row r's chunk c (16 bytes) is kept in slot c ^ swz(r), swz(r) = the bits
-// (r0 ^ r5, r1, r4): the 16 rows of a fragment read then fill all slots of even
-// and of odd rows, free of bank conflicts.
-template <int BM_, int BN_, int WT_, int WC_>
+// Row r's chunk c (16 bytes) is kept in slot c ^ swizzle(r).  A 16-byte read
+// of a wave goes in four phases of 16 lanes, each of all 64 banks (two rows of
+// slots); a phase joins quads of lanes of two neighbouring chunks (0-3, 12-15,
+// 20-23, 24-27 and so on).  With a quad's number q = (q1 q0) in row bits 4 and
+// 5 (channels) or 2 and 3 (tokens), the swizzle bits (q1, row bit 1, q0 ^ q1)
+// from the lowest take both these and 16 lanes in a row to 16 different slots.
+template <int BM_, int BN_, int WT_, int S_>
 struct Q8Tile {
     static constexpr int BM = BM_, BN = BN_;       // tokens, channels
-    static constexpr int WT = WT_, WC = WC_;       // waves along each
-    static constexpr int NW = WT * WC, NTH = NW * 64;
+    static constexpr int NW = 8, NTH = NW * 64;
+    static constexpr int WT = WT_, WC = NW / WT;   // waves along each
+    static constexpr int S = S_;                   // stages
     static constexpr int MT = BM / WT / 16, NC = BN / WC / 16;   // 16-row blocks per wave
-    static constexpr int XBYTES = BM * 128, WBYTES = BN * 128;
+    static constexpr int XROWS = (BM + 63) / 64 * 64;            // whole rounds of the waves' 8-row loads
+    static constexpr int XBYTES = XROWS * 128, WBYTES = BN * 128;
     static constexpr int STAGE = XBYTES + WBYTES;
-    static constexpr int XG = BM / 8 / NW, WG = BN / 8 / NW;     // DMA instructions (8 rows) per wave and tile
-    static_assert(MT % 4 == 0 && NC % 4 == 0, "whole 64-row groups per wave");
-    static_assert(NW % 8 == 0, "a wave's DMA groups share their swizzle");
-    static_assert(BM / 8 % NW == 0 && BN / 8 % NW == 0, "DMA groups split evenly across waves");
+    static constexpr int XG = XROWS / 8 / NW, WG = BN / 8 / NW;  // loads (8 rows) per wave and tile
+    static constexpr int LOADS = XG + WG, FRAGS = MT + NC;
+    static_assert(MT * 16 * WT == BM && NC * 16 * WC == BN && NC % 4 == 0, "whole blocks and 64-channel groups per wave");
+    static_assert(BN % 64 == 0 && S * STAGE <= 160 * 1024 && S >= 2, "ring");
 };
 
-__device__ __forceinline__ int swz_tile(int row) {
-    return ((row ^ (row >> 5)) & 1) | (row & 2) | (((row >> 4) & 1) << 2);
+__device__ __forceinline__ int swizzle(int row, int q0) {   // q0: the position of the quad's bits
+    const int lo = (row >> q0) & 1, hi = (row >> (q0 + 1)) & 1;
+    return hi | (row & 2) | (lo ^ hi) << 2;
 }
 
 struct TileGrid {
-    int tm, tn;   // tiles along the tokens and the channels
+    int tm, tn;    // tiles along the tokens and the channels
+    int ks;        // parts of K
+    int* part;     // int32 sums [ks][T][N] where ks > 1
 };
 
-// Workgroup id -> tile.  Ids go round the XCDs, so XCD x takes the x-th
-// contiguous part of the tile order, in which kGroupM token tiles share a
+// Workgroup id -> part of K and tile.  Ids go round the XCDs, so XCD x takes
+// the x-th contiguous part of the order, in which kGroupM token tiles share a
 // channel tile before the next one: the tiles an XCD works on at one time are
 // a block, whose operands' rows meet in its L2.
 constexpr int kGroupM = 8;
 
-__device__ __forceinline__ void tile_of(int id, const TileGrid& g, int& m, int& n) {
-    const int total = g.tm * g.tn, q = total / kNumXCD, r = total % kNumXCD;
+__device__ __forceinline__ void tile_of(int id, const TileGrid& g, int& part, int& m, int& n) {
+    const int tiles = g.tm * g.tn, total = tiles * g.ks, q = total / kNumXCD, r = total % kNumXCD;
     const int x = id % kNumXCD;
-    const int i = x * q + (x < r ? x : r) + id / kNumXCD;
+    int i = x * q + (x < r ? x : r) + id / kNumXCD;
+    part = i / tiles;
+    i -= part * tiles;
     const int per = kGroupM * g.tn, grp = i / per, rest = i % per;
     const int h = g.tm - grp * kGroupM < kGroupM ? g.tm - grp * kGroupM : kGroupM;
     m = grp * kGroupM + rest % h;
     n = rest / h;
 }
 
-template <typename E, typename G, bool VEC>
+// DMA: rows are 16-byte aligned and go to LDS directly; otherwise through
+// registers, from any address.  VEC: rows of y (and lora) are 16-byte aligned.
+// PART: the sums of a part of K go to the workspace.
+template <typename E, typename G, bool DMA, bool VEC, bool PART>
 __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid) {
-    __shared__ __attribute__((aligned(1024))) char smem[2 * G::STAGE];
+    __shared__ __attribute__((aligned(1024))) char smem[G::S * G::STAGE];
+    constexpr int S = G::S, LOADS = G::LOADS, FRAGS = G::FRAGS;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wt = wave / G::WC, wc = wave % G::WC;
-    int tm, tn;
-    tile_of(blockIdx.x, grid, tm, tn);
+    int part, tm, tn;
+    tile_of(blockIdx.x, grid, part, tm, tn);
     const int64_t t0 = (int64_t)tm * G::BM, n0 = (int64_t)tn * G::BN;
-    const int K = (int)a.K;
-    const int nk = (K + 127) / 128;
+    const int K = (int)a.K, tiles = (K + 127) / 128;
+    const int k_begin = PART ? (int)((int64_t)tiles * part / grid.ks) : 0;
+    const int nk = (PART ? (int)((int64_t)tiles * (part + 1) / grid.ks) : tiles) - k_begin;
 
-    // DMA: lane l moves slot l % 8 of row l / 8 of an 8-row group; the wave's
-    // groups are wave, wave + NW, ...  Rows past the end repeat the last one
-    // (their results are not stored); chunks past K read zeros.
-    const int chunk = ((lane & 7) ^ swz_tile(wave * 8 + (lane >> 3))) * 16;
+    // Loads: lane l moves slot l % 8 of row l / 8 of an 8-row group; the wave's
+    // groups are wave, wave + 8, ..., whose swizzles agree.  Rows past the end
+    // repeat the last one (their results are not stored); chunks past K read
+    // zeros.
+    const int lrow = wave * 8 + (lane >> 3);
+    const int xchunk = ((lane & 7) ^ swizzle(lrow, 2)) * 16, wchunk = ((lane & 7) ^ swizzle(lrow, 4)) * 16;
     int xoff[G::XG], woff[G::WG];
 #pragma unroll
     for (int i = 0; i < G::XG; ++i) {
-        const int r = (wave + i * G::NW) * 8 + (lane >> 3);
-        xoff[i] = (int)(t0 + r < a.T ? r : a.T - 1 - t0) * K + chunk;
+        const int r = lrow + i * G::NW * 8;
+        xoff[i] = (int)(t0 + r < a.T ? r : a.T - 1 - t0) * K + (DMA ? xchunk : 0);
     }
 #pragma unroll
     for (int i = 0; i < G::WG; ++i) {
-        const int r = (wave + i * G::NW) * 8 + (lane >> 3);
-        woff[i] = (int)(n0 + r < a.N ? r : a.N - 1 - n0) * K + chunk;
+        const int r = lrow + i * G::NW * 8;
+        woff[i] = (int)(n0 + r < a.N ? r : a.N - 1 - n0) * K + (DMA ? wchunk : 0);
     }
+    const int8_t* xbase_p = a.xq + t0 * K;
+    const int8_t* wbase_p = a.wq + n0 * K;
     auto resource = [](const void* p) __attribute__((always_inline)) {
         const uint64_t v = reinterpret_cast<uint64_t>(p);
         i32x4_t rs;
@@ -229,39 +264,51 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
         rs[3] = kRsrcWord3;
         return rs;
     };
-    const i32x4_t xr = resource(a.xq + t0 * K), wr = resource(a.wq + n0 * K);
-    auto issue = [&](int kt) __attribute__((always_inline)) {
-        // past the last k-tile: zeros, into a stage that no one reads
-        const bool in = kt * 128 + chunk < K;
-        char* dst = smem + (kt & 1) * G::STAGE + wave * 1024;
+    const i32x4_t xr = resource(xbase_p), wr = resource(wbase_p);
+    i32x4_t held[DMA ? 1 : LOADS];   // the tile on its way through registers
+    // load i of the part's tile j; past the last one: nothing that anyone reads
+    auto issue_one = [&](int j, int stage, int i) __attribute__((always_inline)) {
+        const int k = (k_begin + j) * 128;
+        if (DMA) {
+            const bool in = j < nk && k + (i < G::XG ? xchunk : wchunk) < K;
+            char* dst = smem + stage + wave * 1024 + i * G::NW * 1024;   // the channels' rows follow the tokens'
+            if (i < G::XG)
+                raw_buffer_load_lds(xr, (lds_void_t*)dst, 16, in ? xoff[i < G::XG ? i : 0] : kOutOfRange, k, 0, 0);
+            else
+                raw_buffer_load_lds(wr, (lds_void_t*)dst, 16, in ? woff[i < G::XG ? 0 : i - G::XG] : kOutOfRange, k, 0, 0);
+        } else if (j < nk) {
+            const int8_t* row = i < G::XG ? xbase_p + xoff[i < G::XG ? i : 0] : wbase_p + woff[i < G::XG ? 0 : i - G::XG];
+            const int at = k + (i < G::XG ? xchunk : wchunk);
+            held[DMA ? 0 : i] = k + 128 <= K ? load16(row + at) : load16_tail(row, at, K);
+        }
+    };
+    auto issue = [&](int j, int stage) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < G::XG; ++i)
-            raw_buffer_load_lds(xr, (lds_void_t*)(dst + i * G::NW * 1024), 16, in ? xoff[i] : kOutOfRange, kt * 128, 0, 0);
+        for (int i = 0; i < LOADS; ++i) issue_one(j, stage, i);
+    };
+    auto land = [&](int stage) __attribute__((always_inline)) {   // registers to LDS
+        if (!DMA) {
 #pragma unroll
-        for (int i = 0; i < G::WG; ++i)
-            raw_buffer_load_lds(wr, (lds_void_t*)(dst + G::XBYTES + i * G::NW * 1024), 16, in ? woff[i] : kOutOfRange,
-                                kt * 128, 0, 0);
+            for (int i = 0; i < LOADS; ++i)
+                *reinterpret_cast<i32x4_t*>(smem + stage + wave * 1024 + i * G::NW * 1024 + lane * 16) = held[DMA ? 0 : i];
+        }
     };
 
-    // fragments: lane l reads row 16 ((l % 16) / 4) + l % 4 of a group (+ 4 b
-    // for block b), chunk 4 ks + l / 16
-    const int fr = ((lane & 12) << 2) | (lane & 3), fs = swz_tile(fr);
-    const int fo = fr * 128 + (((lane >> 4) ^ fs) << 4);   // ks = 0; ks = 1 is fo ^ 64
-    const int xbase = wt * G::MT * 16 * 128, wbase = G::XBYTES + wc * G::NC * 16 * 128;
+    // fragments: lane l reads chunk 4 ks + l / 16 of its row
+    const int xrow = lane & 15, wrow = ((lane & 12) << 2) | (lane & 3);
+    const int xfo = (wt * G::MT * 16 + xrow) * 128 + (((lane >> 4) ^ swizzle(xrow, 2)) << 4);   // ks = 0; ks = 1 is ^ 64
+    const int wfo = G::XBYTES + (wc * G::NC * 16 + wrow) * 128 + (((lane >> 4) ^ swizzle(wrow, 4)) << 4);
     i32x4_t acc[G::MT][G::NC];
 #pragma unroll
     for (int m = 0; m < G::MT; ++m)
 #pragma unroll
         for (int c = 0; c < G::NC; ++c) acc[m][c] = {0, 0, 0, 0};
 
-    auto read = [&](int kt, int ks, i32x4_t (&x)[G::MT], i32x4_t (&w)[G::NC]) __attribute__((always_inline)) {
-        const char* st = smem + (kt & 1) * G::STAGE + (fo ^ (ks * 64));
-#pragma unroll
-        for (int c = 0; c < G::NC; ++c)
-            w[c] = *reinterpret_cast<const i32x4_t*>(st + wbase + (c / 4) * 64 * 128 + (c % 4) * 4 * 128);
-#pragma unroll
-        for (int m = 0; m < G::MT; ++m)
-            x[m] = *reinterpret_cast<const i32x4_t*>(st + xbase + (m / 4) * 64 * 128 + (m % 4) * 4 * 128);
+    auto read_one = [&](int stage, int ks, int i, i32x4_t (&x)[G::MT], i32x4_t (&w)[G::NC]) __attribute__((always_inline)) {
+        if (i < G::NC)
+            w[i < G::NC ? i : 0] = *reinterpret_cast<const i32x4_t*>(smem + stage + (wfo ^ (ks * 64)) + (i / 4) * 64 * 128 + (i % 4) * 4 * 128);
+        else
+            x[i < G::NC ? 0 : i - G::NC] = *reinterpret_cast<const i32x4_t*>(smem + stage + (xfo ^ (ks * 64)) + (i - G::NC) * 16 * 128);
     };
     auto mma = [&](const i32x4_t (&x)[G::MT], const i32x4_t (&w)[G::NC]) __attribute__((always_inline)) {
 #pragma unroll
@@ -269,40 +316,66 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
 #pragma unroll
             for (int c = 0; c < G::NC; ++c) acc[m][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[c], x[m], acc[m][c], 0, 0, 0);
     };
-    // one read for every two MFMAs, so that the reads run under the matrix pipe
-    auto interleave = []() __attribute__((always_inline)) {
+    // Reads, and the second step's loads, are spread over the MFMAs: the reads
+    // run under the matrix pipe, and a wave's loads wait their turn at the
+    // CU's one address unit without holding up its MFMAs.
+    constexpr int PER = G::MT * G::NC < FRAGS ? 1 : G::MT * G::NC / FRAGS;   // MFMAs per fragment read
+    auto interleave = [](bool loads) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < G::MT + G::NC; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);   // MFMA
-            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // LDS read
+        for (int i = 0; i < FRAGS; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);   // MFMA
+            if (loads && DMA && i < LOADS) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);   // load
+            __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // LDS read
         }
         __builtin_amdgcn_sched_group_barrier(0x008, G::MT * G::NC, 0);
         __builtin_amdgcn_sched_barrier(0);
     };
 
     // A k-tile is two steps of 64 codes.  While one step's MFMAs run the next
-    // step's fragments are read.  Between them, once per tile: this wave's DMA
-    // of the next tile has landed and its reads of this tile are done; barrier;
-    // then the tile after the next is enqueued into this tile's stage.
+    // step's fragments are read.  Between them, once per tile: this wave's
+    // loads of the next tile have landed and its reads of this tile are done;
+    // barrier; then tile j + S is enqueued into this tile's stage.
     i32x4_t x0[G::MT], w0[G::NC], x1[G::MT], w1[G::NC];
-    issue(0);
-    issue(1);
-    wait_vmcnt<G::XG + G::WG>();
-    __builtin_amdgcn_s_barrier();
-    read(0, 0, x0, w0);
-    for (int kt = 0; kt < nk; ++kt) {
-        read(kt, 1, x1, w1);
-        mma(x0, w0);
-        interleave();
+    if (nk > 0) {
+        if (DMA) {
+#pragma unroll
+            for (int s = 0; s < S; ++s) issue(s, s * G::STAGE);
+            wait_vmcnt<(S - 1) * LOADS>();
+            __builtin_amdgcn_s_barrier();
+        } else {
+            issue(0, 0);
+            land(0);
+            __syncthreads();
+            issue(1, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < FRAGS; ++i) read_one(0, 0, i, x0, w0);
+        int here = 0;   // this tile's stage
+        for (int j = 0; j < nk; ++j) {
+            const int next = here + G::STAGE == S * G::STAGE ? 0 : here + G::STAGE;
+#pragma unroll
+            for (int i = 0; i < FRAGS; ++i) read_one(here, 1, i, x1, w1);
+            mma(x0, w0);
+            interleave(false);
+            if (DMA) {
+                wait_vmcnt<(S - 2) * LOADS>();
+                wait_lgkmcnt0();
+                __builtin_amdgcn_s_barrier();
+            } else {
+                land(next);   // tile j + 1, whose stage's readers passed the last barrier
+                __syncthreads();
+            }
+#pragma unroll
+            for (int i = 0; i < (FRAGS > LOADS ? FRAGS : LOADS); ++i) {
+                if (i < LOADS) issue_one(DMA ? j + S : j + 2, here, i);
+                if (i < FRAGS) read_one(next, 0, i, x0, w0);   // past the last tile: unused
+            }
+            mma(x1, w1);
+            interleave(true);
+            here = next;
+        }
         wait_vmcnt<0>();
-        wait_lgkmcnt0();
-        __builtin_amdgcn_s_barrier();
-        issue(kt + 2);
-        read(kt + 1, 0, x0, w0);   // past the last tile: zeros or an old tile, unused
-        mma(x1, w1);
-        interleave();
     }
-    wait_vmcnt<0>();
 
     // epilogue: token block m of the wave, channels ch .. ch + 15 per lane
     auto epilogue = [&](auto adapter) __attribute__((always_inline)) {
@@ -313,14 +386,27 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
             const int64_t ch = n0 + (wc * G::NC + cg * 4) * 16 + (lane >> 4) * 16;
             if (ch >= a.N) continue;
             Channel cc[16];
-            load_channels(a, ch, cc);
+            if (!PART) load_channels(a, ch, cc);
 #pragma unroll
             for (int m = 0; m < G::MT; ++m) {
-                const int r = lane & 15;
-                const int64_t t = t0 + (wt * G::MT + (m & ~3)) * 16 + (r >> 2) * 16 + (m & 3) * 4 + (r & 3);
+                const int64_t t = t0 + (wt * G::MT + m) * 16 + (lane & 15);
                 if (t >= a.T) continue;
-                const float xs = a.xs[t];
                 const int64_t at = t * a.N + ch;
+                if (PART) {
+                    int* dst = grid.part + (int64_t)part * a.T * a.N + at;
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if (a.N % 4 == 0) {
+                            if (ch + 4 * b < a.N) *reinterpret_cast<i32x4_t*>(dst + 4 * b) = acc[m][cg * 4 + b];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (ch + 4 * b + e < a.N) dst[4 * b + e] = acc[m][cg * 4 + b][e];
+                        }
+                    }
+                    continue;
+                }
+                const float xs = a.xs[t];
 #pragma unroll
                 for (int h = 0; h < 16; h += P) {
                     if (ch + h >= a.N) continue;
@@ -341,22 +427,88 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
             }
         }
     };
-    if (a.g)
+    if (!PART && a.g)
         epilogue(std::true_type{});
     else
         epilogue(std::false_type{});
 }
 
+// The parts of K joined, and the epilogue: 4 channels of one token per thread
+// (one where N is not a multiple of 4).  Integer sums: any order is exact.
+template <typename E, int P>
+__global__ __launch_bounds__(256) void q8_join(MatmulQ8 a, const int* __restrict__ part, int ks) {
+    const int64_t per = a.N / P, all = a.T * a.N;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.T * per; i += (int64_t)gridDim.x * 256) {
+        const int64_t t = i / per, n = (i - t * per) * P, at = t * a.N + n;
+        int v[P];
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[e] = 0;
+        for (int k = 0; k < ks; ++k) {
+            const int* src = part + k * all + at;
+            if (P == 4) {
+                const i32x4_t q = *reinterpret_cast<const i32x4_t*>(src);
+#pragma unroll
+                for (int e = 0; e < P; ++e) v[e] += q[e];
+            } else {
+                v[0] += *src;
+            }
+        }
+        Channel cc[P];
+        load_channels(a, n, cc);
+        const float xs = a.xs[t];
+        E l[P], o[P];
+        if (a.g) __builtin_memcpy(l, static_cast<const E*>(a.lora) + at, sizeof(l));
+#pragma unroll
+        for (int e = 0; e < P; ++e)
+            o[e] = Cvt<E>::from_f(a.g ? finish<true>(v[e], xs, cc[e], Cvt<E>::to_f(l[e])) : finish<false>(v[e], xs, cc[e], 0.0f));
+        __builtin_memcpy(static_cast<E*>(a.y) + at, o, sizeof(o));
+    }
+}
+
+// ------------------------------------------------------------- choice of form
+
+// Tokens and channels of the tile forms.
+constexpr struct { int bm, bn; } kForms[] = {{256, 256}, {192, 256}, {128, 256}, {64, 256}, {128, 128}, {64, 128}};
+constexpr int kNumForms = sizeof(kForms) / sizeof(kForms[0]);
+constexpr int kMaxParts = 16;
+
+struct Q8Plan {
+    int form;   // -1: straight from memory
+    int ks;
+};
+
+Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
+    if (T <= 64 || K < 16) return {-1, 1};
+    if (!dma) return {4, 1};
+    return {0, 1};
+}
+
+size_t plan_bytes(const Q8Plan& p, int64_t T, int64_t N) { return p.ks > 1 ? (size_t)p.ks * T * N * sizeof(int) : 0; }
+
 // ------------------------------------------------------------- launches
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-template <typename E, typename G>
-hipError_t launch_tiles(const MatmulQ8& a, hipStream_t st) {
-    const TileGrid g{(int)((a.T + G::BM - 1) / G::BM), (int)((a.N + G::BN - 1) / G::BN)};
-    const bool vec = a.N % Pack<E>::N == 0 && aligned16(a.y) && aligned16(a.lora);
-    auto k = vec ? q8_tiles<E, G, true> : q8_tiles<E, G, false>;
-    k<<<(unsigned)(g.tm * g.tn), G::NTH, 0, st>>>(a, g);
+template <typename E, typename G, bool DMA>
+hipError_t launch_form(const MatmulQ8& a, int ks, void* workspace, hipStream_t st) {
+    const TileGrid g{(int)((a.T + G::BM - 1) / G::BM), (int)((a.N + G::BN - 1) / G::BN), ks, static_cast<int*>(workspace)};
+    const unsigned wgs = (unsigned)(g.tm * g.tn * ks);
+    if (ks > 1) {
+        q8_tiles<float, G, DMA, false, true><<<wgs, G::NTH, 0, st>>>(a, g);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const int p = a.N % 4 == 0 ? 4 : 1;
+        int64_t blocks = (a.T * (a.N / p) + 255) / 256;
+        if (blocks > 65536) blocks = 65536;
+        if (p == 4)
+            q8_join<E, 4><<<(unsigned)blocks, 256, 0, st>>>(a, g.part, ks);
+        else
+            q8_join<E, 1><<<(unsigned)blocks, 256, 0, st>>>(a, g.part, ks);
+    } else if (a.N % Pack<E>::N == 0 && aligned16(a.y) && aligned16(a.lora)) {
+        q8_tiles<E, G, DMA, true, false><<<wgs, G::NTH, 0, st>>>(a, g);
+    } else {
+        q8_tiles<E, G, DMA, false, false><<<wgs, G::NTH, 0, st>>>(a, g);
+    }
     return hipGetLastError();
 }
 
@@ -382,22 +534,43 @@ hipError_t launch_direct(MatmulQ8 a, hipStream_t st) {
 }
 
 template <typename E>
-hipError_t launch_typed(const MatmulQ8& a, hipStream_t st) {
+hipError_t launch_typed(const MatmulQ8& a, void* workspace, hipStream_t st) {
     const bool dma = a.K % 16 == 0 && aligned16(a.xq) && aligned16(a.wq);
-    if (a.T > 64 && dma) return launch_tiles<E, Q8Tile<256, 256, 2, 4>>(a, st);
-    return launch_direct<E>(a, st);
+    const Q8Plan p = plan_q8(a.T, a.N, a.K, dma);
+    if (p.form < 0) return launch_direct<E>(a, st);
+    if (!dma) {
+        if (p.form == 4) return launch_form<E, Q8Tile<128, 128, 4, 2>, false>(a, p.ks, workspace, st);
+        return launch_form<E, Q8Tile<64, 128, 4, 2>, false>(a, p.ks, workspace, st);
+    }
+    switch (p.form) {
+        case 0: return launch_form<E, Q8Tile<256, 256, 2, 2>, true>(a, p.ks, workspace, st);
+        case 1: return launch_form<E, Q8Tile<192, 256, 2, 2>, true>(a, p.ks, workspace, st);
+        case 2: return launch_form<E, Q8Tile<128, 256, 2, 3>, true>(a, p.ks, workspace, st);
+        case 3: return launch_form<E, Q8Tile<64, 256, 2, 3>, true>(a, p.ks, workspace, st);
+        case 4: return launch_form<E, Q8Tile<128, 128, 4, 4>, true>(a, p.ks, workspace, st);
+        default: return launch_form<E, Q8Tile<64, 128, 4, 4>, true>(a, p.ks, workspace, st);
+    }
 }
 
 }  // namespace
 
-size_t matmul_q8_workspace_bytes(int64_t T, int64_t N, int64_t K) { return 0; }
+size_t matmul_q8_workspace_bytes(int64_t T, int64_t N, int64_t K) {
+    // the codes' alignment is known only at the call
+    size_t most = 0;
+    for (int dma = 0; dma < 2; ++dma) {
+        if (dma && K % 16 != 0) continue;
+        const size_t b = plan_bytes(plan_q8(T, N, K, dma), T, N);
+        most = b > most ? b : most;
+    }
+    return align_up(most, 256);
+}
 
 hipError_t launch_matmul_q8(const MatmulQ8& a, int dtype, void* workspace, hipStream_t stream) {
     if (a.T == 0) return hipSuccess;
     switch (dtype) {
-        case kF32: return launch_typed<float>(a, stream);
-        case kBF16: return launch_typed<bf16_t>(a, stream);
-        default: return launch_typed<f16_t>(a, stream);
+        case kF32: return launch_typed<float>(a, workspace, stream);
+        case kBF16: return launch_typed<bf16_t>(a, workspace, stream);
+        default: return launch_typed<f16_t>(a, workspace, stream);
     }
 }
 
