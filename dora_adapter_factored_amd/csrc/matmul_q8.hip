@@ -159,7 +159,9 @@ constexpr int kNumCU = 256;
 constexpr int kNumXCD = 8;
 
 // BM tokens x BN channels per workgroup of 8 waves, k-tiles of 128 codes
-// (whole 128-byte rows) of both operands in an LDS ring of S stages.
+// (whole 128-byte rows) of both operands in an LDS ring of S stages.  The
+// waves form KG groups: one, or two that each take 64 codes of every k-tile
+// and add their sums at the end, for tiles too small to feed eight waves.
 //
 // Rows of an LDS tile keep their order.  Of a 64-channel group, the 16-row
 // MFMA block b takes rows 16 (r / 4) + 4 b + r % 4, r = 0..15: lane l's
@@ -174,20 +176,27 @@ constexpr int kNumXCD = 8;
 // 20-23, 24-27 and so on).  With a quad's number q = (q1 q0) in row bits 4 and
 // 5 (channels) or 2 and 3 (tokens), the swizzle bits (q1, row bit 1, q0 ^ q1)
 // from the lowest take both these and 16 lanes in a row to 16 different slots.
-template <int BM_, int BN_, int WT_, int S_>
+//
+// D > 0: tiles come through registers, D of them on their way at a time, for
+// codes whose rows are not 4-byte aligned; otherwise by LDS DMA.
+template <int BM_, int BN_, int WT_, int KG_, int S_, int D_ = 0>
 struct Q8Tile {
     static constexpr int BM = BM_, BN = BN_;       // tokens, channels
     static constexpr int NW = 8, NTH = NW * 64;
-    static constexpr int WT = WT_, WC = NW / WT;   // waves along each
-    static constexpr int S = S_;                   // stages
+    static constexpr int KG = KG_;
+    static constexpr int WT = WT_, WC = NW / KG / WT;            // waves of a group along each
+    static constexpr int S = S_, D = D_;
     static constexpr int MT = BM / WT / 16, NC = BN / WC / 16;   // 16-row blocks per wave
     static constexpr int XROWS = (BM + 63) / 64 * 64;            // whole rounds of the waves' 8-row loads
     static constexpr int XBYTES = XROWS * 128, WBYTES = BN * 128;
     static constexpr int STAGE = XBYTES + WBYTES;
+    static constexpr int LDS = S * STAGE;
     static constexpr int XG = XROWS / 8 / NW, WG = BN / 8 / NW;  // loads (8 rows) per wave and tile
     static constexpr int LOADS = XG + WG, FRAGS = MT + NC;
     static_assert(MT * 16 * WT == BM && NC * 16 * WC == BN && NC % 4 == 0, "whole blocks and 64-channel groups per wave");
-    static_assert(BN % 64 == 0 && S * STAGE <= 160 * 1024 && S >= 2, "ring");
+    static_assert(BN % 64 == 0 && LDS <= 160 * 1024 && S >= 2 && (S - 1) * LOADS < 64, "ring");
+    static_assert(KG == 1 || (KG == 2 && BM * BN * 4 <= LDS), "the second group's sums pass through the ring");
+    static_assert(D == 0 || S == 2, "tiles through registers wait there, not in LDS");
 };
 
 __device__ __forceinline__ int swizzle(int row, int q0) {   // q0: the position of the quad's bits
@@ -219,16 +228,16 @@ __device__ __forceinline__ void tile_of(int id, const TileGrid& g, int& part, in
     n = rest / h;
 }
 
-// DMA: rows are 16-byte aligned and go to LDS directly; otherwise through
-// registers, from any address.  VEC: rows of y (and lora) are 16-byte aligned.
-// PART: the sums of a part of K go to the workspace.
-template <typename E, typename G, bool DMA, bool VEC, bool PART>
+// VEC: rows of y (and lora) are 16-byte aligned.  PART: the sums of a part of
+// K go to the workspace.
+template <typename E, typename G, bool VEC, bool PART>
 __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid) {
-    __shared__ __attribute__((aligned(1024))) char smem[G::S * G::STAGE];
-    constexpr int S = G::S, LOADS = G::LOADS, FRAGS = G::FRAGS;
+    __shared__ __attribute__((aligned(1024))) char smem[G::LDS];
+    constexpr int S = G::S, D = G::D, LOADS = G::LOADS, FRAGS = G::FRAGS;
+    constexpr bool DMA = D == 0;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wt = wave / G::WC, wc = wave % G::WC;
+    const int kg = wave / (G::WT * G::WC), wt = wave / G::WC % G::WT, wc = wave % G::WC;
     int part, tm, tn;
     tile_of(blockIdx.x, grid, part, tm, tn);
     const int64_t t0 = (int64_t)tm * G::BM, n0 = (int64_t)tn * G::BN;
@@ -239,7 +248,8 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
     // Loads: lane l moves slot l % 8 of row l / 8 of an 8-row group; the wave's
     // groups are wave, wave + 8, ..., whose swizzles agree.  Rows past the end
     // repeat the last one (their results are not stored); chunks past K read
-    // zeros.
+    // zeros.  A chunk that crosses K holds the next row's first codes (past
+    // the operand's end: zeros, by the buffer's size), which mask() removes.
     const int lrow = wave * 8 + (lane >> 3);
     const int xchunk = ((lane & 7) ^ swizzle(lrow, 2)) * 16, wchunk = ((lane & 7) ^ swizzle(lrow, 4)) * 16;
     int xoff[G::XG], woff[G::WG];
@@ -255,21 +265,21 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
     }
     const int8_t* xbase_p = a.xq + t0 * K;
     const int8_t* wbase_p = a.wq + n0 * K;
-    auto resource = [](const void* p) __attribute__((always_inline)) {
+    auto resource = [](const void* p, int64_t bytes) __attribute__((always_inline)) {
         const uint64_t v = reinterpret_cast<uint64_t>(p);
         i32x4_t rs;
         rs[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)v);
         rs[1] = __builtin_amdgcn_readfirstlane((int)(uint32_t)(v >> 32));
-        rs[2] = 0x7fffffff;
+        rs[2] = __builtin_amdgcn_readfirstlane((int)(bytes < 0x7fffffff ? bytes : 0x7fffffff));
         rs[3] = kRsrcWord3;
         return rs;
     };
-    const i32x4_t xr = resource(xbase_p), wr = resource(wbase_p);
-    i32x4_t held[DMA ? 1 : LOADS];   // the tile on its way through registers
+    const i32x4_t xr = resource(xbase_p, (a.T - t0) * K), wr = resource(wbase_p, (a.N - n0) * K);
+    i32x4_t held[DMA ? 1 : D][DMA ? 1 : LOADS];   // tiles on their way through registers
     // load i of the part's tile j; past the last one: nothing that anyone reads
-    auto issue_one = [&](int j, int stage, int i) __attribute__((always_inline)) {
+    auto issue_one = [&](int j, int stage, int slot, int i) __attribute__((always_inline)) {
         const int k = (k_begin + j) * 128;
-        if (DMA) {
+        if constexpr (DMA) {
             const bool in = j < nk && k + (i < G::XG ? xchunk : wchunk) < K;
             char* dst = smem + stage + wave * 1024 + i * G::NW * 1024;   // the channels' rows follow the tokens'
             if (i < G::XG)
@@ -279,18 +289,18 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
         } else if (j < nk) {
             const int8_t* row = i < G::XG ? xbase_p + xoff[i < G::XG ? i : 0] : wbase_p + woff[i < G::XG ? 0 : i - G::XG];
             const int at = k + (i < G::XG ? xchunk : wchunk);
-            held[DMA ? 0 : i] = k + 128 <= K ? load16(row + at) : load16_tail(row, at, K);
+            held[slot][i] = k + 128 <= K ? load16(row + at) : load16_tail(row, at, K);
         }
     };
-    auto issue = [&](int j, int stage) __attribute__((always_inline)) {
+    auto issue = [&](int j, int stage, int slot) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < LOADS; ++i) issue_one(j, stage, i);
+        for (int i = 0; i < LOADS; ++i) issue_one(j, stage, slot, i);
     };
-    auto land = [&](int stage) __attribute__((always_inline)) {   // registers to LDS
-        if (!DMA) {
+    auto land = [&](int stage, int slot) __attribute__((always_inline)) {   // registers to LDS
+        if constexpr (!DMA) {
 #pragma unroll
             for (int i = 0; i < LOADS; ++i)
-                *reinterpret_cast<i32x4_t*>(smem + stage + wave * 1024 + i * G::NW * 1024 + lane * 16) = held[DMA ? 0 : i];
+                *reinterpret_cast<i32x4_t*>(smem + stage + wave * 1024 + i * G::NW * 1024 + lane * 16) = held[slot][i];
         }
     };
 
@@ -309,6 +319,19 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
             w[i < G::NC ? i : 0] = *reinterpret_cast<const i32x4_t*>(smem + stage + (wfo ^ (ks * 64)) + (i / 4) * 64 * 128 + (i % 4) * 4 * 128);
         else
             x[i < G::NC ? 0 : i - G::NC] = *reinterpret_cast<const i32x4_t*>(smem + stage + (xfo ^ (ks * 64)) + (i - G::NC) * 16 * 128);
+    };
+    // the last k-tile's codes past K out of the channels' fragments
+    const bool ragged = DMA && K % 16 != 0 && k_begin + nk == tiles;
+    auto mask = [&](int j, int ks, i32x4_t (&w)[G::NC]) __attribute__((always_inline)) {
+        if (DMA && ragged && j == nk - 1) {
+            const int left = K - (k_begin + j) * 128 - (ks * 4 + (lane >> 4)) * 16;   // a multiple of 4
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+                const int keep = 4 * d < left ? -1 : 0;
+#pragma unroll
+                for (int c = 0; c < G::NC; ++c) w[c][d] &= keep;
+            }
+        }
     };
     auto mma = [&](const i32x4_t (&x)[G::MT], const i32x4_t (&w)[G::NC]) __attribute__((always_inline)) {
 #pragma unroll
@@ -331,50 +354,89 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    // A k-tile is two steps of 64 codes.  While one step's MFMAs run the next
-    // step's fragments are read.  Between them, once per tile: this wave's
-    // loads of the next tile have landed and its reads of this tile are done;
-    // barrier; then tile j + S is enqueued into this tile's stage.
+    // A k-tile is two steps of 64 codes (with two groups: one step of each).
+    // While one step's MFMAs run the next step's fragments are read.  Once per
+    // tile, before its last step: this wave's loads of the next tile have
+    // landed and its reads of this tile are done; barrier; then tile j + S (in
+    // registers: j + 1 + D) is enqueued into what this tile (tile j + 1) held.
     i32x4_t x0[G::MT], w0[G::NC], x1[G::MT], w1[G::NC];
+    constexpr int UNROLL = DMA ? 1 : D;   // registers are indexed by constants
     if (nk > 0) {
-        if (DMA) {
+        if constexpr (DMA) {
 #pragma unroll
-            for (int s = 0; s < S; ++s) issue(s, s * G::STAGE);
+            for (int s = 0; s < S; ++s) issue(s, s * G::STAGE, 0);
             wait_vmcnt<(S - 1) * LOADS>();
             __builtin_amdgcn_s_barrier();
         } else {
-            issue(0, 0);
-            land(0);
+#pragma unroll
+            for (int s = 0; s < D; ++s) issue(s, 0, s);
+            land(0, 0);
+            issue(D, 0, 0);
             __syncthreads();
-            issue(1, 0);
         }
+        const int ks0 = G::KG == 1 ? 0 : kg;
 #pragma unroll
-        for (int i = 0; i < FRAGS; ++i) read_one(0, 0, i, x0, w0);
+        for (int i = 0; i < FRAGS; ++i) read_one(0, ks0, i, x0, w0);
+        mask(0, ks0, w0);
         int here = 0;   // this tile's stage
-        for (int j = 0; j < nk; ++j) {
-            const int next = here + G::STAGE == S * G::STAGE ? 0 : here + G::STAGE;
+        for (int j0 = 0; j0 < nk; j0 += UNROLL) {
 #pragma unroll
-            for (int i = 0; i < FRAGS; ++i) read_one(here, 1, i, x1, w1);
-            mma(x0, w0);
-            interleave(false);
-            if (DMA) {
-                wait_vmcnt<(S - 2) * LOADS>();
-                wait_lgkmcnt0();
-                __builtin_amdgcn_s_barrier();
-            } else {
-                land(next);   // tile j + 1, whose stage's readers passed the last barrier
-                __syncthreads();
-            }
+            for (int d = 0; d < UNROLL; ++d) {
+                const int j = j0 + d;
+                if (UNROLL > 1 && j >= nk) break;
+                const int next = here + G::STAGE == G::LDS ? 0 : here + G::STAGE, slot = (d + 1) % UNROLL;
+                if constexpr (G::KG == 1) {
 #pragma unroll
-            for (int i = 0; i < (FRAGS > LOADS ? FRAGS : LOADS); ++i) {
-                if (i < LOADS) issue_one(DMA ? j + S : j + 2, here, i);
-                if (i < FRAGS) read_one(next, 0, i, x0, w0);   // past the last tile: unused
+                    for (int i = 0; i < FRAGS; ++i) read_one(here, 1, i, x1, w1);
+                    mma(x0, w0);
+                    interleave(false);
+                    mask(j, 1, w1);
+                } else {
+#pragma unroll
+                    for (int m = 0; m < G::MT; ++m) x1[m] = x0[m];
+#pragma unroll
+                    for (int c = 0; c < G::NC; ++c) w1[c] = w0[c];
+                }
+                if constexpr (DMA) {
+                    wait_vmcnt<(S - 2) * LOADS>();
+                    wait_lgkmcnt0();
+                    __builtin_amdgcn_s_barrier();
+                } else {
+                    land(next, slot);   // the readers of that stage's last tile passed the last barrier
+                    __syncthreads();
+                }
+#pragma unroll
+                for (int i = 0; i < (FRAGS > LOADS ? FRAGS : LOADS); ++i) {
+                    if (i < LOADS) issue_one(DMA ? j + S : j + 1 + D, here, slot, i);
+                    if (i < FRAGS) read_one(next, ks0, i, x0, w0);   // past the last tile: unused
+                }
+                mma(x1, w1);
+                interleave(true);
+                mask(j + 1, ks0, w0);
+                here = next;
             }
-            mma(x1, w1);
-            interleave(true);
-            here = next;
         }
         wait_vmcnt<0>();
+    }
+    if constexpr (G::KG == 2) {   // the second group's sums to the first
+        __syncthreads();
+        char* sums = smem + (wt * G::WC + wc) * G::MT * G::NC * 1024 + lane * 16;
+        if (kg == 1) {
+#pragma unroll
+            for (int m = 0; m < G::MT; ++m)
+#pragma unroll
+                for (int c = 0; c < G::NC; ++c) *reinterpret_cast<i32x4_t*>(sums + (m * G::NC + c) * 1024) = acc[m][c];
+        }
+        __syncthreads();
+        if (kg == 1) return;
+#pragma unroll
+        for (int m = 0; m < G::MT; ++m)
+#pragma unroll
+            for (int c = 0; c < G::NC; ++c) {
+                const i32x4_t v = *reinterpret_cast<const i32x4_t*>(sums + (m * G::NC + c) * 1024);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][c][e] += v[e];
+            }
     }
 
     // epilogue: token block m of the wave, channels ch .. ch + 15 per lane
@@ -467,19 +529,16 @@ __global__ __launch_bounds__(256) void q8_join(MatmulQ8 a, const int* __restrict
 
 // ------------------------------------------------------------- choice of form
 
-// Tokens and channels of the tile forms.
-constexpr struct { int bm, bn; } kForms[] = {{256, 256}, {192, 256}, {128, 256}, {64, 256}, {128, 128}, {64, 128}};
-constexpr int kNumForms = sizeof(kForms) / sizeof(kForms[0]);
-constexpr int kMaxParts = 16;
+constexpr int kDirect = -1;
 
 struct Q8Plan {
-    int form;   // -1: straight from memory
-    int ks;
+    int form;   // kDirect, or a tile form
+    int ks;     // parts of K
 };
 
 Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
-    if (T <= 64 || K < 16) return {-1, 1};
-    if (!dma) return {4, 1};
+    if (T <= 64 || K < 16) return {kDirect, 1};
+    if (!dma) return {T * N > 512 * 4096 ? 4 : 6, 1};
     return {0, 1};
 }
 
@@ -487,14 +546,14 @@ size_t plan_bytes(const Q8Plan& p, int64_t T, int64_t N) { return p.ks > 1 ? (si
 
 // ------------------------------------------------------------- launches
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+inline bool aligned_to(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-template <typename E, typename G, bool DMA>
+template <typename E, typename G>
 hipError_t launch_form(const MatmulQ8& a, int ks, void* workspace, hipStream_t st) {
     const TileGrid g{(int)((a.T + G::BM - 1) / G::BM), (int)((a.N + G::BN - 1) / G::BN), ks, static_cast<int*>(workspace)};
     const unsigned wgs = (unsigned)(g.tm * g.tn * ks);
     if (ks > 1) {
-        q8_tiles<float, G, DMA, false, true><<<wgs, G::NTH, 0, st>>>(a, g);
+        q8_tiles<float, G, false, true><<<wgs, G::NTH, 0, st>>>(a, g);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const int p = a.N % 4 == 0 ? 4 : 1;
@@ -504,10 +563,10 @@ hipError_t launch_form(const MatmulQ8& a, int ks, void* workspace, hipStream_t s
             q8_join<E, 4><<<(unsigned)blocks, 256, 0, st>>>(a, g.part, ks);
         else
             q8_join<E, 1><<<(unsigned)blocks, 256, 0, st>>>(a, g.part, ks);
-    } else if (a.N % Pack<E>::N == 0 && aligned16(a.y) && aligned16(a.lora)) {
-        q8_tiles<E, G, DMA, true, false><<<wgs, G::NTH, 0, st>>>(a, g);
+    } else if (a.N % Pack<E>::N == 0 && aligned_to(a.y, 16) && aligned_to(a.lora, 16)) {
+        q8_tiles<E, G, true, false><<<wgs, G::NTH, 0, st>>>(a, g);
     } else {
-        q8_tiles<E, G, DMA, false, false><<<wgs, G::NTH, 0, st>>>(a, g);
+        q8_tiles<E, G, false, false><<<wgs, G::NTH, 0, st>>>(a, g);
     }
     return hipGetLastError();
 }
@@ -535,20 +594,23 @@ hipError_t launch_direct(MatmulQ8 a, hipStream_t st) {
 
 template <typename E>
 hipError_t launch_typed(const MatmulQ8& a, void* workspace, hipStream_t st) {
-    const bool dma = a.K % 16 == 0 && aligned16(a.xq) && aligned16(a.wq);
+    const bool dma = a.K % 4 == 0 && aligned_to(a.xq, 4) && aligned_to(a.wq, 4);
     const Q8Plan p = plan_q8(a.T, a.N, a.K, dma);
-    if (p.form < 0) return launch_direct<E>(a, st);
+    if (p.form == kDirect) return launch_direct<E>(a, st);
     if (!dma) {
-        if (p.form == 4) return launch_form<E, Q8Tile<128, 128, 4, 2>, false>(a, p.ks, workspace, st);
-        return launch_form<E, Q8Tile<64, 128, 4, 2>, false>(a, p.ks, workspace, st);
+        if (p.form == 4) return launch_form<E, Q8Tile<128, 128, 4, 1, 2, 3>>(a, p.ks, workspace, st);
+        return launch_form<E, Q8Tile<64, 64, 4, 2, 2, 8>>(a, p.ks, workspace, st);
     }
     switch (p.form) {
-        case 0: return launch_form<E, Q8Tile<256, 256, 2, 2>, true>(a, p.ks, workspace, st);
-        case 1: return launch_form<E, Q8Tile<192, 256, 2, 2>, true>(a, p.ks, workspace, st);
-        case 2: return launch_form<E, Q8Tile<128, 256, 2, 3>, true>(a, p.ks, workspace, st);
-        case 3: return launch_form<E, Q8Tile<64, 256, 2, 3>, true>(a, p.ks, workspace, st);
-        case 4: return launch_form<E, Q8Tile<128, 128, 4, 4>, true>(a, p.ks, workspace, st);
-        default: return launch_form<E, Q8Tile<64, 128, 4, 4>, true>(a, p.ks, workspace, st);
+        case 0: return launch_form<E, Q8Tile<256, 256, 2, 1, 2>>(a, p.ks, workspace, st);
+        case 1: return launch_form<E, Q8Tile<192, 256, 2, 1, 2>>(a, p.ks, workspace, st);
+        case 2: return launch_form<E, Q8Tile<128, 256, 2, 1, 3>>(a, p.ks, workspace, st);
+        case 3: return launch_form<E, Q8Tile<64, 256, 2, 1, 4>>(a, p.ks, workspace, st);
+        case 4: return launch_form<E, Q8Tile<128, 128, 4, 1, 5>>(a, p.ks, workspace, st);
+        case 5: return launch_form<E, Q8Tile<64, 128, 4, 1, 6>>(a, p.ks, workspace, st);
+        case 6: return launch_form<E, Q8Tile<64, 64, 4, 2, 8>>(a, p.ks, workspace, st);
+        case 7: return launch_form<E, Q8Tile<128, 64, 4, 2, 6>>(a, p.ks, workspace, st);
+        default: return launch_form<E, Q8Tile<64, 64, 4, 2, 4>>(a, p.ks, workspace, st);
     }
 }
 
@@ -558,7 +620,7 @@ size_t matmul_q8_workspace_bytes(int64_t T, int64_t N, int64_t K) {
     // the codes' alignment is known only at the call
     size_t most = 0;
     for (int dma = 0; dma < 2; ++dma) {
-        if (dma && K % 16 != 0) continue;
+        if (dma && K % 4 != 0) continue;
         const size_t b = plan_bytes(plan_q8(T, N, K, dma), T, N);
         most = b > most ? b : most;
     }
