@@ -276,9 +276,16 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
     };
     const i32x4_t xr = resource(xbase_p, (a.T - t0) * K), wr = resource(wbase_p, (a.N - n0) * K);
     i32x4_t held[DMA ? 1 : D][DMA ? 1 : LOADS];   // tiles on their way through registers
-    // load i of the part's tile j; past the last one: nothing that anyone reads
+    // Each XCD starts its walk over K at its own place, so that rows of one
+    // pitch are not all asked for the same columns at once; within an XCD the
+    // walks stay together, which its L2 lives on.
+    const int rot = (int)((unsigned)(blockIdx.x % kNumXCD) * (unsigned)nk / kNumXCD);
+    auto tile_at = [&](int j) __attribute__((always_inline)) {   // the j-th k-tile of the walk
+        return k_begin + (j + rot < nk ? j + rot : j + rot - nk);
+    };
+    // load i of the walk's tile j; past the last one: nothing that anyone reads
     auto issue_one = [&](int j, int stage, int slot, int i) __attribute__((always_inline)) {
-        const int k = (k_begin + j) * 128;
+        const int k = tile_at(j) * 128;
         if constexpr (DMA) {
             const bool in = j < nk && k + (i < G::XG ? xchunk : wchunk) < K;
             char* dst = smem + stage + wave * 1024 + i * G::NW * 1024;   // the channels' rows follow the tokens'
@@ -321,10 +328,10 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
             x[i < G::NC ? 0 : i - G::NC] = *reinterpret_cast<const i32x4_t*>(smem + stage + (xfo ^ (ks * 64)) + (i - G::NC) * 16 * 128);
     };
     // the last k-tile's codes past K out of the channels' fragments
-    const bool ragged = DMA && K % 16 != 0 && k_begin + nk == tiles;
+    const bool ragged = DMA && K % 16 != 0;
     auto mask = [&](int j, int ks, i32x4_t (&w)[G::NC]) __attribute__((always_inline)) {
-        if (DMA && ragged && j == nk - 1) {
-            const int left = K - (k_begin + j) * 128 - (ks * 4 + (lane >> 4)) * 16;   // a multiple of 4
+        if (DMA && ragged && tile_at(j) == tiles - 1) {
+            const int left = K - (tiles - 1) * 128 - (ks * 4 + (lane >> 4)) * 16;   // a multiple of 4
 #pragma unroll
             for (int d = 0; d < 4; ++d) {
                 const int keep = 4 * d < left ? -1 : 0;
