@@ -29,26 +29,27 @@ __device__ __forceinline__ i32x4_t load16(const int8_t* p) {
     return v;
 }
 
+// v without its first n bytes, zeros after them.
+__device__ __forceinline__ i32x4_t drop_bytes(const i32x4_t& v, int n) {
+    uint64_t lo = (uint32_t)v[0] | (uint64_t)(uint32_t)v[1] << 32, hi = (uint32_t)v[2] | (uint64_t)(uint32_t)v[3] << 32;
+    const int bits = 8 * n;
+    if (n >= 16) lo = hi = 0;
+    else if (n >= 8) lo = hi >> (bits - 64), hi = 0;
+    else if (n > 0) lo = lo >> bits | hi << (64 - bits), hi >>= bits;
+    return i32x4_t{(int)(uint32_t)lo, (int)(uint32_t)(lo >> 32), (int)(uint32_t)hi, (int)(uint32_t)(hi >> 32)};
+}
+
 // Bytes k .. k + 15 of a row of K, zeros past its end: the last 16 bytes of
 // the row moved down, so that nothing outside the row is read.
 __device__ __forceinline__ i32x4_t load16_tail(const int8_t* row, int k, int K) {
-    i32x4_t v = {0, 0, 0, 0};
     if (K < 16) {
+        i32x4_t v = {0, 0, 0, 0};
         for (int b = 0; b < 16; ++b)
             if (k + b < K) v[b / 4] |= (int)(uint8_t)row[k + b] << (8 * (b % 4));
         return v;
     }
-    const int at = k < K - 16 ? k : K - 16, skip = 8 * (k - at);   // bits
-    const i32x4_t r = load16(row + at);
-    uint64_t lo = (uint32_t)r[0] | (uint64_t)(uint32_t)r[1] << 32, hi = (uint32_t)r[2] | (uint64_t)(uint32_t)r[3] << 32;
-    if (skip >= 128) lo = hi = 0;
-    else if (skip >= 64) lo = hi >> (skip - 64), hi = 0;
-    else if (skip > 0) lo = lo >> skip | hi << (64 - skip), hi >>= skip;
-    v[0] = (int)(uint32_t)lo;
-    v[1] = (int)(uint32_t)(lo >> 32);
-    v[2] = (int)(uint32_t)hi;
-    v[3] = (int)(uint32_t)(hi >> 32);
-    return v;
+    const int at = k < K - 16 ? k : K - 16;
+    return drop_bytes(load16(row + at), k - at);
 }
 
 // One result: its scales, the composition, the bias.  Contraction is off so
@@ -92,70 +93,129 @@ __device__ __forceinline__ float finish(int acc, float xs, const Channel& c, flo
     return v + c.bias;
 }
 
-// 16 channels x 16 C tokens per workgroup, the waves taking 128-byte columns
-// of K in turn straight from memory into the MFMA operands; the waves' sums
-// are added through LDS.
-template <typename E, int C>
-__global__ __launch_bounds__(kWaves * 64) void q8_direct(MatmulQ8 a) {
-    __shared__ int red[kWaves][C][256];
+// One token: kRows channels per workgroup on the vector units.  The weight's
+// bytes are all that counts, and a load takes 1 KB of one channel's row, whole
+// lines only, where the MFMA layout of q8_direct asks for 64 bytes of each of
+// 16 rows, which holds a CU to about 22 GB/s.  Wave w takes every eighth KB of
+// the rows from the w-th; lanes, then waves are summed at the end.  8192 x
+// 8192: 13.6 us, 4.9 TB/s (q8_direct 15.1); 28672 x 8192: 39.1 us, 6.0 TB/s
+// (42.6); 5120 x 27648: 27.5 us (39.5); two channels per workgroup 46.8 us and
+// eight 43.4 at 28672 x 8192.
+constexpr int kRows = 4;
+
+template <typename E>
+__global__ __launch_bounds__(kWaves * 64) void q8_one_token(MatmulQ8 a) {
+    __shared__ int red[kWaves][kRows];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * 16 * C;
+    const int64_t n0 = (int64_t)blockIdx.x * kRows;
+    const int K = (int)a.K;
+    int acc[kRows] = {};
+    auto step = [&](int k, auto tail) __attribute__((always_inline)) {
+        constexpr bool TAIL = decltype(tail)::value;
+        i32x4_t w[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {   // channels past the end repeat the last one; their results are not stored
+            const int8_t* row = a.wq + (n0 + r < a.N ? n0 + r : a.N - 1) * K;
+            w[r] = TAIL ? load16_tail(row, k, K) : load16(row + k);
+        }
+        const i32x4_t x = TAIL ? load16_tail(a.xq, k, K) : load16(a.xq + k);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) acc[r] = __builtin_amdgcn_sdot4(w[r][d], x[d], acc[r], false);
+    };
+    int k0 = wave * 1024;
+#pragma unroll 2
+    for (; k0 + 1024 <= K; k0 += kWaves * 1024) step(k0 + lane * 16, std::false_type{});
+    if (k0 < K) step(k0 + lane * 16, std::true_type{});
+    // the lanes' sums: two steps in which a lane hands half of its values over
+    // and keeps the others, after which lane l holds channel l / 16
+    const bool up5 = lane & 32, up4 = lane & 16;
+    int v0 = (up5 ? acc[2] : acc[0]) + __shfl_xor(up5 ? acc[0] : acc[2], 32);
+    const int v1 = (up5 ? acc[3] : acc[1]) + __shfl_xor(up5 ? acc[1] : acc[3], 32);
+    v0 = (up4 ? v1 : v0) + __shfl_xor(up4 ? v0 : v1, 16);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v0 += __shfl_xor(v0, o);
+    if (lane % 16 == 0) red[wave][lane / 16] = v0;
+    __syncthreads();
+    const int64_t n = n0 + threadIdx.x;
+    if (threadIdx.x >= kRows || n >= a.N) return;
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += red[w][threadIdx.x];
+    Channel cc[1];
+    load_channels(a, n, cc);
+    const float y = a.g ? finish<true>(sum, a.xs[0], cc[0], Cvt<E>::to_f(static_cast<const E*>(a.lora)[n]))
+                        : finish<false>(sum, a.xs[0], cc[0], 0.0f);
+    static_cast<E*>(a.y)[n] = Cvt<E>::from_f(y);
+}
+
+// 16 channels x 16 tokens per workgroup, the waves taking 128-byte columns of
+// K in turn straight from memory into the MFMA operands; the waves' sums are
+// added through LDS.  For few tokens and channels, where tiles through LDS
+// would leave most CUs without work (12 x 1024 x 5120: 7.0 us, 64 x 64 tiles
+// in 4 parts 10.4), for rows of fewer than 16 codes, and for up to 16 tokens
+// of codes whose rows are not 4-byte aligned.
+template <typename E>
+__global__ __launch_bounds__(kWaves * 64) void q8_direct(MatmulQ8 a) {
+    __shared__ int red[kWaves][256];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t n0 = (int64_t)blockIdx.x * 16, t0 = (int64_t)blockIdx.y * 16;
     // rows past the end repeat the last one; their results are not stored
     const int64_t nr = n0 + (lane & 15) < a.N ? n0 + (lane & 15) : a.N - 1;
+    const int64_t tr = t0 + (lane & 15) < a.T ? t0 + (lane & 15) : a.T - 1;
     const int kl = (lane >> 4) * 32;
     const int K = (int)a.K;
     const int8_t* wp = a.wq + nr * K;
-    const int8_t* xp[C];
-    i32x4_t acc[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-        const int64_t t = t0 + c * 16 + (lane & 15);
-        xp[c] = a.xq + (t < a.T ? t : a.T - 1) * K;
-        acc[c] = {0, 0, 0, 0};
-    }
+    const int8_t* xp = a.xq + tr * K;
+    i32x4_t acc = {0, 0, 0, 0};
     const int full = K / 128;
-    for (int kb = wave; kb < full; kb += kWaves) {
+    // U columns at a time, all their loads before the first MFMA
+    auto columns = [&](int kb, auto u) __attribute__((always_inline)) {
+        constexpr int U = decltype(u)::value;
+        i32x4_t w[U][2], x[U][2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int k = kb * 128 + kl + j * 16;
-            const i32x4_t w = load16(wp + k);
+        for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, load16(xp[c] + k), acc[c], 0, 0, 0);
-        }
-    }
+            for (int j = 0; j < 2; ++j) {
+                const int k = (kb + i * kWaves) * 128 + kl + j * 16;
+                w[i][j] = load16(wp + k);
+                x[i][j] = load16(xp + k);
+            }
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i][j], x[i][j], acc, 0, 0, 0);
+    };
+    int kb = wave;
+    for (; kb + 3 * kWaves < full; kb += 4 * kWaves) columns(kb, std::integral_constant<int, 4>{});
+    for (; kb < full; kb += kWaves) columns(kb, std::integral_constant<int, 1>{});
     if (full % kWaves == wave && full * 128 < K) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int k = full * 128 + kl + j * 16;
-            const i32x4_t w = load16_tail(wp, k, K);
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-                acc[c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w, load16_tail(xp[c], k, K), acc[c], 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(load16_tail(wp, k, K), load16_tail(xp, k, K), acc, 0, 0, 0);
         }
     }
-#pragma unroll
-    for (int c = 0; c < C; ++c) *reinterpret_cast<i32x4_t*>(&red[wave][c][lane * 4]) = acc[c];
+    *reinterpret_cast<i32x4_t*>(&red[wave][lane * 4]) = acc;
     __syncthreads();
-    for (int o = threadIdx.x; o < C * 256; o += kWaves * 64) {
-        const int c = o >> 8, tok = (o >> 4) & 15, ch = o & 15;
-        const int64_t t = t0 + c * 16 + tok, n = n0 + ch;
-        if (t >= a.T || n >= a.N) continue;
-        const int src = ((ch >> 2) * 16 + tok) * 4 + (ch & 3);
-        int v = 0;
+    if (threadIdx.x >= 256) return;
+    const int tok = threadIdx.x >> 4, ch = threadIdx.x & 15;
+    const int64_t t = t0 + tok, n = n0 + ch;
+    if (t >= a.T || n >= a.N) return;
+    const int src = ((ch >> 2) * 16 + tok) * 4 + (ch & 3);
+    int v = 0;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) v += red[w][c][src];
-        Channel cc[1];
-        load_channels(a, n, cc);
-        const float r = a.g ? finish<true>(v, a.xs[t], cc[0], Cvt<E>::to_f(static_cast<const E*>(a.lora)[t * a.N + n]))
-                            : finish<false>(v, a.xs[t], cc[0], 0.0f);
-        static_cast<E*>(a.y)[t * a.N + n] = Cvt<E>::from_f(r);
-    }
+    for (int w = 0; w < kWaves; ++w) v += red[w][src];
+    Channel cc[1];
+    load_channels(a, n, cc);
+    const float r = a.g ? finish<true>(v, a.xs[t], cc[0], Cvt<E>::to_f(static_cast<const E*>(a.lora)[t * a.N + n]))
+                        : finish<false>(v, a.xs[t], cc[0], 0.0f);
+    static_cast<E*>(a.y)[t * a.N + n] = Cvt<E>::from_f(r);
 }
 
 // ------------------------------------------------------------- tiles through LDS
 
-constexpr int kNumCU = 256;
 constexpr int kNumXCD = 8;
 
 // BM tokens x BN channels per workgroup of 8 waves, k-tiles of 128 codes
@@ -207,8 +267,16 @@ __device__ __forceinline__ int swizzle(int row, int q0) {   // q0: the position 
 struct TileGrid {
     int tm, tn;    // tiles along the tokens and the channels
     int ks;        // parts of K
-    int* part;     // int32 sums [ks][T][N] where ks > 1
+    int* part;     // where ks > 1: the parts' int32 sums, as part_at() lays them out
 };
+
+// The sums of one MFMA block of one part, 16 bytes a lane: blocks of a wave,
+// waves of a tile, tiles, parts.
+template <typename G>
+__device__ __forceinline__ i32x4_t* part_at(const TileGrid& g, int part, int tm, int tn, int wave, int m, int c) {
+    const int64_t tile = ((int64_t)part * g.tn + tn) * g.tm + tm;
+    return reinterpret_cast<i32x4_t*>(g.part) + (((tile * (G::NW / G::KG) + wave) * G::MT + m) * G::NC + c) * 64;
+}
 
 // Workgroup id -> part of K and tile.  Ids go round the XCDs, so XCD x takes
 // the x-th contiguous part of the order, in which kGroupM token tiles share a
@@ -228,6 +296,46 @@ __device__ __forceinline__ void tile_of(int id, const TileGrid& g, int& part, in
     n = rest / h;
 }
 
+// Results of wave (wt, wc) of the tile at (t0, n0), token blocks m_begin ..
+// m_end - 1: lane l has token l % 16 of a block and the 16 channels from 16 (l
+// / 16) of each 64-channel group, four of them in sums(m, group, 0 .. 3) each.
+template <typename E, typename G, bool VEC, bool ADAPTER, typename Sums>
+__device__ __forceinline__ void store_results(const MatmulQ8& a, int64_t t0, int64_t n0, int wt, int wc, int m_begin, int m_end,
+                                              Sums sums) {
+    constexpr int P = VEC ? Pack<E>::N : 1;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int cg = 0; cg < G::NC / 4; ++cg) {
+        const int64_t ch = n0 + (wc * G::NC + cg * 4) * 16 + (lane >> 4) * 16;
+        if (ch >= a.N) continue;
+        Channel cc[16];
+        load_channels(a, ch, cc);
+#pragma unroll
+        for (int m = m_begin; m < m_end; ++m) {
+            const int64_t t = t0 + (wt * G::MT + m) * 16 + (lane & 15);
+            if (t >= a.T) continue;
+            const int64_t at = t * a.N + ch;
+            const float xs = a.xs[t];
+#pragma unroll
+            for (int h = 0; h < 16; h += P) {
+                if (ch + h >= a.N) continue;
+                if (VEC) {
+                    Pack<E> l, o;
+                    if (ADAPTER) l = load_pack(static_cast<const E*>(a.lora) + at + h);
+#pragma unroll
+                    for (int e = 0; e < P; ++e)
+                        o.e[e] = Cvt<E>::from_f(finish<ADAPTER>(sums(m, cg, (h + e) / 4)[(h + e) % 4], xs, cc[h + e],
+                                                                ADAPTER ? Cvt<E>::to_f(l.e[e]) : 0.0f));
+                    *reinterpret_cast<u32x4_t*>(static_cast<E*>(a.y) + at + h) = o.u;
+                } else {
+                    const float l = ADAPTER ? Cvt<E>::to_f(static_cast<const E*>(a.lora)[at + h]) : 0.0f;
+                    static_cast<E*>(a.y)[at + h] = Cvt<E>::from_f(finish<ADAPTER>(sums(m, cg, h / 4)[h % 4], xs, cc[h], l));
+                }
+            }
+        }
+    }
+}
+
 // VEC: rows of y (and lora) are 16-byte aligned.  PART: the sums of a part of
 // K go to the workspace.
 template <typename E, typename G, bool VEC, bool PART>
@@ -243,7 +351,8 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
     const int64_t t0 = (int64_t)tm * G::BM, n0 = (int64_t)tn * G::BN;
     const int K = (int)a.K, tiles = (K + 127) / 128;
     const int k_begin = PART ? (int)((int64_t)tiles * part / grid.ks) : 0;
-    const int nk = (PART ? (int)((int64_t)tiles * (part + 1) / grid.ks) : tiles) - k_begin;
+    // through registers the walk is over whole tiles, and a ragged last one follows it
+    const int nk = DMA ? (PART ? (int)((int64_t)tiles * (part + 1) / grid.ks) : tiles) - k_begin : K / 128;
 
     // Loads: lane l moves slot l % 8 of row l / 8 of an 8-row group; the wave's
     // groups are wave, wave + 8, ..., whose swizzles agree.  Rows past the end
@@ -283,6 +392,9 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
     auto tile_at = [&](int j) __attribute__((always_inline)) {   // the j-th k-tile of the walk
         return k_begin + (j + rot < nk ? j + rot : j + rot - nk);
     };
+    auto row_of = [&](int i) __attribute__((always_inline)) {
+        return i < G::XG ? xbase_p + xoff[i < G::XG ? i : 0] : wbase_p + woff[i < G::XG ? 0 : i - G::XG];
+    };
     // load i of the walk's tile j; past the last one: nothing that anyone reads
     auto issue_one = [&](int j, int stage, int slot, int i) __attribute__((always_inline)) {
         const int k = tile_at(j) * 128;
@@ -293,21 +405,22 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
                 raw_buffer_load_lds(xr, (lds_void_t*)dst, 16, in ? xoff[i < G::XG ? i : 0] : kOutOfRange, k, 0, 0);
             else
                 raw_buffer_load_lds(wr, (lds_void_t*)dst, 16, in ? woff[i < G::XG ? 0 : i - G::XG] : kOutOfRange, k, 0, 0);
-        } else if (j < nk) {
-            const int8_t* row = i < G::XG ? xbase_p + xoff[i < G::XG ? i : 0] : wbase_p + woff[i < G::XG ? 0 : i - G::XG];
-            const int at = k + (i < G::XG ? xchunk : wchunk);
-            held[slot][i] = k + 128 <= K ? load16(row + at) : load16_tail(row, at, K);
+        } else {   // past the last tile the first again, which land() turns to zeros: no branch round a load
+            held[slot][i] = load16(row_of(i) + (j < nk ? k : 0) + (i < G::XG ? xchunk : wchunk));
         }
     };
     auto issue = [&](int j, int stage, int slot) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < LOADS; ++i) issue_one(j, stage, slot, i);
     };
-    auto land = [&](int stage, int slot) __attribute__((always_inline)) {   // registers to LDS
+    auto put = [&](int stage, int i, const i32x4_t& v) __attribute__((always_inline)) {
+        *reinterpret_cast<i32x4_t*>(smem + stage + wave * 1024 + i * G::NW * 1024 + lane * 16) = v;
+    };
+    auto land = [&](int j, int stage, int slot) __attribute__((always_inline)) {   // registers to LDS
         if constexpr (!DMA) {
+            const int keep = j < nk ? -1 : 0;
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i)
-                *reinterpret_cast<i32x4_t*>(smem + stage + wave * 1024 + i * G::NW * 1024 + lane * 16) = held[slot][i];
+            for (int i = 0; i < LOADS; ++i) put(stage, i, held[slot][i] & keep);
         }
     };
 
@@ -368,6 +481,16 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
     // registers: j + 1 + D) is enqueued into what this tile (tile j + 1) held.
     i32x4_t x0[G::MT], w0[G::NC], x1[G::MT], w1[G::NC];
     constexpr int UNROLL = DMA ? 1 : D;   // registers are indexed by constants
+    i32x4_t last[DMA ? 1 : LOADS];   // through registers: the ragged last tile, at hand from the start
+    if (!DMA) {
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int at = K / 128 * 128 + (i < G::XG ? xchunk : wchunk);
+            last[DMA ? 0 : i] = load16(row_of(i) + (at < K - 16 ? at : K - 16));
+        }
+    }
+    const int ks0 = G::KG == 1 ? 0 : kg;
+    int here = 0;   // this tile's stage
     if (nk > 0) {
         if constexpr (DMA) {
 #pragma unroll
@@ -377,20 +500,17 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
         } else {
 #pragma unroll
             for (int s = 0; s < D; ++s) issue(s, 0, s);
-            land(0, 0);
+            land(0, 0, 0);
             issue(D, 0, 0);
             __syncthreads();
         }
-        const int ks0 = G::KG == 1 ? 0 : kg;
 #pragma unroll
         for (int i = 0; i < FRAGS; ++i) read_one(0, ks0, i, x0, w0);
         mask(0, ks0, w0);
-        int here = 0;   // this tile's stage
         for (int j0 = 0; j0 < nk; j0 += UNROLL) {
 #pragma unroll
             for (int d = 0; d < UNROLL; ++d) {
-                const int j = j0 + d;
-                if (UNROLL > 1 && j >= nk) break;
+                const int j = j0 + d;   // past the last tile: zeros
                 const int next = here + G::STAGE == G::LDS ? 0 : here + G::STAGE, slot = (d + 1) % UNROLL;
                 if constexpr (G::KG == 1) {
 #pragma unroll
@@ -409,7 +529,7 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
                     wait_lgkmcnt0();
                     __builtin_amdgcn_s_barrier();
                 } else {
-                    land(next, slot);   // the readers of that stage's last tile passed the last barrier
+                    land(j + 1, next, slot);   // the readers of that stage's last tile passed the last barrier
                     __syncthreads();
                 }
 #pragma unroll
@@ -423,7 +543,22 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
                 here = next;
             }
         }
-        wait_vmcnt<0>();
+        if (DMA) wait_vmcnt<0>();
+    }
+    if (!DMA && K % 128 != 0) {
+        const int other = G::STAGE - here;   // its readers passed the last barrier
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) {
+            const int at = K / 128 * 128 + (i < G::XG ? xchunk : wchunk);
+            put(other, i, drop_bytes(last[DMA ? 0 : i], at > K - 16 ? at - (K - 16) : 0));
+        }
+        __syncthreads();
+#pragma unroll
+        for (int ks = ks0; ks < (G::KG == 1 ? 2 : ks0 + 1); ++ks) {
+#pragma unroll
+            for (int i = 0; i < FRAGS; ++i) read_one(other, ks, i, x0, w0);
+            mma(x0, w0);
+        }
     }
     if constexpr (G::KG == 2) {   // the second group's sums to the first
         __syncthreads();
@@ -446,110 +581,138 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
             }
     }
 
-    // epilogue: token block m of the wave, channels ch .. ch + 15 per lane
-    auto epilogue = [&](auto adapter) __attribute__((always_inline)) {
-        constexpr bool ADAPTER = decltype(adapter)::value;
-        constexpr int P = VEC ? Pack<E>::N : 1;
+    if constexpr (PART) {
 #pragma unroll
-        for (int cg = 0; cg < G::NC / 4; ++cg) {
-            const int64_t ch = n0 + (wc * G::NC + cg * 4) * 16 + (lane >> 4) * 16;
-            if (ch >= a.N) continue;
-            Channel cc[16];
-            if (!PART) load_channels(a, ch, cc);
+        for (int m = 0; m < G::MT; ++m)
 #pragma unroll
-            for (int m = 0; m < G::MT; ++m) {
-                const int64_t t = t0 + (wt * G::MT + m) * 16 + (lane & 15);
-                if (t >= a.T) continue;
-                const int64_t at = t * a.N + ch;
-                if (PART) {
-                    int* dst = grid.part + (int64_t)part * a.T * a.N + at;
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        if (a.N % 4 == 0) {
-                            if (ch + 4 * b < a.N) *reinterpret_cast<i32x4_t*>(dst + 4 * b) = acc[m][cg * 4 + b];
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (ch + 4 * b + e < a.N) dst[4 * b + e] = acc[m][cg * 4 + b][e];
-                        }
-                    }
-                    continue;
-                }
-                const float xs = a.xs[t];
-#pragma unroll
-                for (int h = 0; h < 16; h += P) {
-                    if (ch + h >= a.N) continue;
-                    if (VEC) {
-                        Pack<E> l, o;
-                        if (ADAPTER) l = load_pack(static_cast<const E*>(a.lora) + at + h);
-#pragma unroll
-                        for (int e = 0; e < P; ++e)
-                            o.e[e] = Cvt<E>::from_f(finish<ADAPTER>(acc[m][cg * 4 + (h + e) / 4][(h + e) % 4], xs, cc[h + e],
-                                                                    ADAPTER ? Cvt<E>::to_f(l.e[e]) : 0.0f));
-                        *reinterpret_cast<u32x4_t*>(static_cast<E*>(a.y) + at + h) = o.u;
-                    } else {
-                        const float l = ADAPTER ? Cvt<E>::to_f(static_cast<const E*>(a.lora)[at + h]) : 0.0f;
-                        static_cast<E*>(a.y)[at + h] =
-                            Cvt<E>::from_f(finish<ADAPTER>(acc[m][cg * 4 + h / 4][h % 4], xs, cc[h], l));
-                    }
-                }
-            }
-        }
-    };
-    if (!PART && a.g)
-        epilogue(std::true_type{});
-    else
-        epilogue(std::false_type{});
+            for (int c = 0; c < G::NC; ++c) part_at<G>(grid, part, tm, tn, wt * G::WC + wc, m, c)[lane] = acc[m][c];
+    } else {
+        if (a.g)
+            store_results<E, G, VEC, true>(a, t0, n0, wt, wc, 0, G::MT, [&](int m, int cg, int b) { return acc[m][cg * 4 + b]; });
+        else
+            store_results<E, G, VEC, false>(a, t0, n0, wt, wc, 0, G::MT, [&](int m, int cg, int b) { return acc[m][cg * 4 + b]; });
+    }
 }
 
-// The parts of K joined, and the epilogue: 4 channels of one token per thread
-// (one where N is not a multiple of 4).  Integer sums: any order is exact.
-template <typename E, int P>
-__global__ __launch_bounds__(256) void q8_join(MatmulQ8 a, const int* __restrict__ part, int ks) {
-    const int64_t per = a.N / P, all = a.T * a.N;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.T * per; i += (int64_t)gridDim.x * 256) {
-        const int64_t t = i / per, n = (i - t * per) * P, at = t * a.N + n;
-        int v[P];
+// The parts of K joined, and the epilogue: a wave for each token block of a
+// tile's wave.  Integer sums: any order is exact.
+template <typename E, typename G, bool VEC>
+__global__ __launch_bounds__(256) void q8_join(MatmulQ8 a, TileGrid grid) {
+    const int lane = threadIdx.x & 63;
+    constexpr int PER = G::NW / G::KG * G::MT;   // waves per tile
+    const int id = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * 4 + (threadIdx.x >> 6)));
+    const int tile = id / PER, rest = id % PER, wave = rest / G::MT, m = rest % G::MT;
+    const int tm = tile % grid.tm, tn = tile / grid.tm;
+    if (tn >= grid.tn) return;
+    i32x4_t sum[G::NC];
 #pragma unroll
-        for (int e = 0; e < P; ++e) v[e] = 0;
-        for (int k = 0; k < ks; ++k) {
-            const int* src = part + k * all + at;
-            if (P == 4) {
-                const i32x4_t q = *reinterpret_cast<const i32x4_t*>(src);
+    for (int c = 0; c < G::NC; ++c) sum[c] = {0, 0, 0, 0};
+    for (int p = 0; p < grid.ks; ++p) {
 #pragma unroll
-                for (int e = 0; e < P; ++e) v[e] += q[e];
-            } else {
-                v[0] += *src;
-            }
+        for (int c = 0; c < G::NC; ++c) {
+            const i32x4_t v = part_at<G>(grid, p, tm, tn, wave, m, c)[lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[c][e] += v[e];
         }
-        Channel cc[P];
-        load_channels(a, n, cc);
-        const float xs = a.xs[t];
-        E l[P], o[P];
-        if (a.g) __builtin_memcpy(l, static_cast<const E*>(a.lora) + at, sizeof(l));
-#pragma unroll
-        for (int e = 0; e < P; ++e)
-            o[e] = Cvt<E>::from_f(a.g ? finish<true>(v[e], xs, cc[e], Cvt<E>::to_f(l[e])) : finish<false>(v[e], xs, cc[e], 0.0f));
-        __builtin_memcpy(static_cast<E*>(a.y) + at, o, sizeof(o));
     }
+    const int64_t t0 = (int64_t)tm * G::BM, n0 = (int64_t)tn * G::BN;
+    if (a.g)
+        store_results<E, G, VEC, true>(a, t0, n0, wave / G::WC, wave % G::WC, m, m + 1, [&](int, int cg, int b) { return sum[cg * 4 + b]; });
+    else
+        store_results<E, G, VEC, false>(a, t0, n0, wave / G::WC, wave % G::WC, m, m + 1, [&](int, int cg, int b) { return sum[cg * 4 + b]; });
 }
 
 // ------------------------------------------------------------- choice of form
 
-constexpr int kDirect = -1;
+// The tile forms, by what they cost: a workgroup's time per k-tile in ns where
+// it has the chip nearly to itself and where `slots` of them fill it (two of
+// the small ones fit a CU; up to one a CU they do not slow each other).
+// Measured on MI355X at K = 8192, T = 64 .. 2048, N = 4096 .. 28672.
+struct Q8Form {
+    int bm, bn, slots, ns_empty, ns_full;
+};
+constexpr Q8Form kForms[] = {
+    {256, 256, 256, 1240, 1700}, {192, 256, 256, 1080, 1330}, {128, 256, 256, 740, 970},
+    {128, 128, 256, 470, 660},   {64, 128, 512, 440, 780},    {64, 64, 512, 286, 520},
+};
+constexpr int kNumForms = sizeof(kForms) / sizeof(kForms[0]);
+typedef Q8Tile<256, 256, 2, 1, 2> Form0;
+typedef Q8Tile<192, 256, 2, 1, 2> Form1;
+typedef Q8Tile<128, 256, 2, 1, 3> Form2;
+typedef Q8Tile<128, 128, 4, 1, 5> Form3;
+typedef Q8Tile<64, 128, 4, 1, 3> Form4;
+typedef Q8Tile<64, 64, 4, 2, 4> Form5;
+// through registers
+constexpr int kRegsBig = kNumForms, kRegsSmall = kNumForms + 1;
+typedef Q8Tile<128, 128, 4, 1, 2, 3> FormR0;
+typedef Q8Tile<64, 64, 4, 2, 2, 4> FormR1;
+
+constexpr int kDirect = -1, kOneToken = -2;
+constexpr int kMaxParts = 16;
 
 struct Q8Plan {
-    int form;   // kDirect, or a tile form
+    int form;   // a tile form, kDirect or kOneToken
     int ks;     // parts of K
 };
 
-Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
-    if (T <= 64 || K < 16) return {kDirect, 1};
-    if (!dma) return {T * N > 512 * 4096 ? 4 : 6, 1};
-    return {0, 1};
+size_t plan_bytes(const Q8Plan& p, int64_t T, int64_t N) {
+    if (p.ks == 1) return 0;
+    const Q8Form& f = kForms[p.form];
+    return (size_t)((T + f.bm - 1) / f.bm) * ((N + f.bn - 1) / f.bn) * f.bm * f.bn * sizeof(int) * p.ks;
 }
 
-size_t plan_bytes(const Q8Plan& p, int64_t T, int64_t N) { return p.ks > 1 ? (size_t)p.ks * T * N * sizeof(int) : 0; }
+// The form and number of parts of least cost.  A round of workgroups costs its
+// k-tiles; a launch about 5 us, of which the loads' first latency and the
+// epilogue are most; parts that have to be joined one more launch (3 us) and
+// their bytes written and read again (0.23 us for each MB).  At 333 x 5120 x
+// 27648 this takes 128 x 256 tiles in 4 parts (67 us; without parts 88), at
+// 2048 x 5120 x 5120 192 x 256 tiles (58.5 us; 256 x 256 65.4, 128 x 256
+// 80.9), at 512 x 8192 x 8192 128 x 128 (42.1 us; 128 x 256 54.9, 64 x 128
+// 54.4).
+int64_t cost_q8(int form, int ks, int64_t T, int64_t N, int64_t K) {
+    const Q8Form& f = kForms[form];
+    const int64_t wgs = ((T + f.bm - 1) / f.bm) * ((N + f.bn - 1) / f.bn) * ks, nk = ((K + 127) / 128 + ks - 1) / ks;
+    const int64_t full = wgs / f.slots, rest = wgs % f.slots;
+    int64_t ns = full * f.ns_full;
+    if (rest > 0) ns += f.slots > 256 ? (rest > 256 ? f.ns_full : f.ns_empty) : f.ns_empty + (f.ns_full - f.ns_empty) * rest / 256;
+    ns *= nk;
+    const int64_t read = N * K / 6300;   // the weight at 6.3 TB/s
+    ns = 5000 + (ns > read ? ns : read);
+    if (ks > 1) ns += 3000 + (int64_t)plan_bytes({form, ks}, T, N) / 4400;
+    return ns;
+}
+
+// 16 channels a workgroup straight from memory, for up to 16 tokens: what a
+// CU's workgroups read at 22.5 GB/s, more with x's rows.
+int64_t cost_direct(int64_t T, int64_t N, int64_t K) {
+    const int64_t rounds = (N + 16 * 256 - 1) / (16 * 256);
+    return 2500 + rounds * 16 * K * (420 + T * T) / 420 * 2 / 45;
+}
+
+Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
+    if (T == 1) return {kOneToken, 1};
+    if ((T <= 16 && !dma) || K < 16) return {kDirect, 1};
+    if (!dma) {
+        // rounds of 256 workgroups: 64 x 64 tiles cost 0.44 us a k-tile, 128 x
+        // 128 about 1.1 (100 x 4099 x 4099: 19.3 us against 35.4; 2000 x 4099
+        // x 4099: 150 against 121)
+        auto rounds = [&](int64_t b) { return (((T + b - 1) / b) * ((N + b - 1) / b) + 255) / 256; };
+        return {rounds(64) * 2 <= rounds(128) * 5 ? kRegsSmall : kRegsBig, 1};
+    }
+    Q8Plan best{kDirect, 1};
+    int64_t least = T <= 16 ? cost_direct(T, N, K) : INT64_MAX;
+    for (int f = 0; f < kNumForms; ++f)
+        for (int ks = 1; ks <= kMaxParts && ks * 2 <= (K + 127) / 128 + 1; ++ks) {
+            // parts are for tiles that leave CUs idle
+            if (ks > 1 && ((T + kForms[f].bm - 1) / kForms[f].bm) * ((N + kForms[f].bn - 1) / kForms[f].bn) * ks > kForms[f].slots * 2) break;
+            const int64_t c = cost_q8(f, ks, T, N, K);
+            if (c < least) {
+                least = c;
+                best = {f, ks};
+            }
+        }
+    return best;
+}
 
 // ------------------------------------------------------------- launches
 
@@ -559,22 +722,24 @@ template <typename E, typename G>
 hipError_t launch_form(const MatmulQ8& a, int ks, void* workspace, hipStream_t st) {
     const TileGrid g{(int)((a.T + G::BM - 1) / G::BM), (int)((a.N + G::BN - 1) / G::BN), ks, static_cast<int*>(workspace)};
     const unsigned wgs = (unsigned)(g.tm * g.tn * ks);
-    if (ks > 1) {
-        q8_tiles<float, G, false, true><<<wgs, G::NTH, 0, st>>>(a, g);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        const int p = a.N % 4 == 0 ? 4 : 1;
-        int64_t blocks = (a.T * (a.N / p) + 255) / 256;
-        if (blocks > 65536) blocks = 65536;
-        if (p == 4)
-            q8_join<E, 4><<<(unsigned)blocks, 256, 0, st>>>(a, g.part, ks);
-        else
-            q8_join<E, 1><<<(unsigned)blocks, 256, 0, st>>>(a, g.part, ks);
-    } else if (a.N % Pack<E>::N == 0 && aligned_to(a.y, 16) && aligned_to(a.lora, 16)) {
-        q8_tiles<E, G, true, false><<<wgs, G::NTH, 0, st>>>(a, g);
-    } else {
-        q8_tiles<E, G, false, false><<<wgs, G::NTH, 0, st>>>(a, g);
+    const bool vec = a.N % Pack<E>::N == 0 && aligned_to(a.y, 16) && aligned_to(a.lora, 16);
+    if constexpr (G::D == 0) {
+        if (ks > 1) {
+            q8_tiles<float, G, false, true><<<wgs, G::NTH, 0, st>>>(a, g);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+            const unsigned blocks = (unsigned)((g.tm * g.tn * (G::NW / G::KG * G::MT) + 3) / 4);
+            if (vec)
+                q8_join<E, G, true><<<blocks, 256, 0, st>>>(a, g);
+            else
+                q8_join<E, G, false><<<blocks, 256, 0, st>>>(a, g);
+            return hipGetLastError();
+        }
     }
+    if (vec)
+        q8_tiles<E, G, true, false><<<wgs, G::NTH, 0, st>>>(a, g);
+    else
+        q8_tiles<E, G, false, false><<<wgs, G::NTH, 0, st>>>(a, g);
     return hipGetLastError();
 }
 
@@ -589,10 +754,7 @@ hipError_t launch_direct(MatmulQ8 a, hipStream_t st) {
         a.xs = all.xs + t;
         a.lora = all.lora ? static_cast<const E*>(all.lora) + t * all.N : nullptr;
         a.y = static_cast<E*>(all.y) + t * all.N;
-        if (a.T <= 16)
-            q8_direct<E, 1><<<dim3(gx, 1), kWaves * 64, 0, st>>>(a);
-        else
-            q8_direct<E, 4><<<dim3(gx, (unsigned)((a.T + 63) / 64)), kWaves * 64, 0, st>>>(a);
+        q8_direct<E><<<dim3(gx, (unsigned)((a.T + 15) / 16)), kWaves * 64, 0, st>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -603,21 +765,20 @@ template <typename E>
 hipError_t launch_typed(const MatmulQ8& a, void* workspace, hipStream_t st) {
     const bool dma = a.K % 4 == 0 && aligned_to(a.xq, 4) && aligned_to(a.wq, 4);
     const Q8Plan p = plan_q8(a.T, a.N, a.K, dma);
-    if (p.form == kDirect) return launch_direct<E>(a, st);
-    if (!dma) {
-        if (p.form == 4) return launch_form<E, Q8Tile<128, 128, 4, 1, 2, 3>>(a, p.ks, workspace, st);
-        return launch_form<E, Q8Tile<64, 64, 4, 2, 2, 8>>(a, p.ks, workspace, st);
+    if (p.form == kOneToken) {
+        q8_one_token<E><<<(unsigned)((a.N + kRows - 1) / kRows), kWaves * 64, 0, st>>>(a);
+        return hipGetLastError();
     }
+    if (p.form == kDirect) return launch_direct<E>(a, st);
     switch (p.form) {
-        case 0: return launch_form<E, Q8Tile<256, 256, 2, 1, 2>>(a, p.ks, workspace, st);
-        case 1: return launch_form<E, Q8Tile<192, 256, 2, 1, 2>>(a, p.ks, workspace, st);
-        case 2: return launch_form<E, Q8Tile<128, 256, 2, 1, 3>>(a, p.ks, workspace, st);
-        case 3: return launch_form<E, Q8Tile<64, 256, 2, 1, 4>>(a, p.ks, workspace, st);
-        case 4: return launch_form<E, Q8Tile<128, 128, 4, 1, 5>>(a, p.ks, workspace, st);
-        case 5: return launch_form<E, Q8Tile<64, 128, 4, 1, 6>>(a, p.ks, workspace, st);
-        case 6: return launch_form<E, Q8Tile<64, 64, 4, 2, 8>>(a, p.ks, workspace, st);
-        case 7: return launch_form<E, Q8Tile<128, 64, 4, 2, 6>>(a, p.ks, workspace, st);
-        default: return launch_form<E, Q8Tile<64, 64, 4, 2, 4>>(a, p.ks, workspace, st);
+        case 0: return launch_form<E, Form0>(a, p.ks, workspace, st);
+        case 1: return launch_form<E, Form1>(a, p.ks, workspace, st);
+        case 2: return launch_form<E, Form2>(a, p.ks, workspace, st);
+        case 3: return launch_form<E, Form3>(a, p.ks, workspace, st);
+        case 4: return launch_form<E, Form4>(a, p.ks, workspace, st);
+        case 5: return launch_form<E, Form5>(a, p.ks, workspace, st);
+        case kRegsBig: return launch_form<E, FormR0>(a, 1, workspace, st);
+        default: return launch_form<E, FormR1>(a, 1, workspace, st);
     }
 }
 
