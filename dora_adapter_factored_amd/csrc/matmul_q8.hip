@@ -607,13 +607,10 @@ __global__ __launch_bounds__(256) void q8_join(MatmulQ8 a, TileGrid grid) {
     i32x4_t sum[G::NC];
 #pragma unroll
     for (int c = 0; c < G::NC; ++c) sum[c] = {0, 0, 0, 0};
+#pragma unroll 4
     for (int p = 0; p < grid.ks; ++p) {
 #pragma unroll
-        for (int c = 0; c < G::NC; ++c) {
-            const i32x4_t v = part_at<G>(grid, p, tm, tn, wave, m, c)[lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[c][e] += v[e];
-        }
+        for (int c = 0; c < G::NC; ++c) sum[c] += part_at<G>(grid, p, tm, tn, wave, m, c)[lane];
     }
     const int64_t t0 = (int64_t)tm * G::BM, n0 = (int64_t)tn * G::BN;
     if (a.g)

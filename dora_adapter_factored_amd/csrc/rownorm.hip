@@ -32,63 +32,79 @@ constexpr uint32_t kInfBits = 0x7f800000u;
 // 127 / a would leave the fp32 range there.  The error is below 2^-119.
 constexpr uint32_t kTinyBits = (uint32_t)(127 - 119) << 23;
 
-// N consecutive elements in one access (16 bytes, or one element where rows
-// or pointers are not 16-byte aligned), kept as loaded.
-template <typename E, int N> struct Elems {
+// Rows go in packs of 16 bytes.  Aligned rows (AL: pointers and row pitch
+// multiples of 16 bytes) hold whole packs; in others a pack is read and
+// written at its element's alignment, which the memory pipe splits (element
+// by element it took 2.5 times as long at 2048 x 5121), and the last one may
+// be partial: elements past the row's end read 0 and are not written.
+template <typename E, bool AL>
+__device__ __forceinline__ Pack<E> load_row(const E* p, int64_t left) {
+    constexpr int N = Pack<E>::N;
     Pack<E> k;
-    __device__ __forceinline__ void load(const E* p) { k = load_pack(p); }
-    __device__ __forceinline__ float operator[](int e) const { return Cvt<E>::to_f(k.e[e]); }
-};
-template <typename E> struct Elems<E, 1> {
-    E k;
-    __device__ __forceinline__ void load(const E* p) { k = *p; }
-    __device__ __forceinline__ float operator[](int) const { return Cvt<E>::to_f(k); }
-};
-
-template <typename E, int N>
-__device__ __forceinline__ void store_n(E* p, const float (&v)[N]) {
-    if constexpr (N == 1) {
-        *p = Cvt<E>::from_f(v[0]);
+    if (AL) {
+        k = load_pack(p);
+    } else if (left >= N) {
+        __builtin_memcpy(&k.u, p, 16);
     } else {
-        Pack<E> k;
 #pragma unroll
-        for (int e = 0; e < N; ++e) k.e[e] = Cvt<E>::from_f(v[e]);
+        for (int e = 0; e < N; ++e) k.e[e] = e < left ? p[e] : Cvt<E>::from_f(0.0f);
+    }
+    return k;
+}
+
+template <typename E, bool AL, int N>
+__device__ __forceinline__ void store_row(E* p, const float (&v)[N], int64_t left) {
+    static_assert(N == Pack<E>::N, "a pack");
+    Pack<E> k;
+#pragma unroll
+    for (int e = 0; e < N; ++e) k.e[e] = Cvt<E>::from_f(v[e]);
+    if (AL) {
         store_pack_stream(p, k);
+    } else if (left >= N) {
+        __builtin_memcpy(p, &k.u, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < left) p[e] = k.e[e];
     }
 }
 
-// N column scales / weights as fp32.
-template <typename W, int N>
-__device__ __forceinline__ void load_w(const W* w, int64_t col, float (&v)[N]) {
-    constexpr int M = N * sizeof(W) > 16 ? 4 : N;   // fp32 scales beside 16-bit elements take two accesses
+template <typename E>
+__device__ __forceinline__ float at(const Pack<E>& k, int e) {
+    return Cvt<E>::to_f(k.e[e]);
+}
+
+// N weights (of the row's type) or column scales (fp32) as fp32.
+template <typename W, bool AL, int N>
+__device__ __forceinline__ void load_w(const W* w, int64_t left, float (&v)[N]) {
+    constexpr int M = Pack<W>::N;
 #pragma unroll
     for (int h = 0; h < N; h += M) {
-        Elems<W, M> t;
-        t.load(w + col + h);
+        const Pack<W> k = load_row<W, AL>(w + h, left - h);
 #pragma unroll
-        for (int e = 0; e < M; ++e) v[h + e] = t[e];
+        for (int e = 0; e < M; ++e) v[h + e] = at(k, e);
     }
 }
 
 // N codes: rint(p inv) packed into bytes.  |p inv| <= 127 up to one rounding,
 // which rint takes back to 127.
-template <int N>
-__device__ __forceinline__ void store_codes(int8_t* q, const float (&p)[N], float inv) {
+template <bool AL, int N>
+__device__ __forceinline__ void store_codes(int8_t* q, const float (&p)[N], float inv, int64_t left) {
     int c[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) c[e] = (int)rintf(p[e] * inv);
-    if constexpr (N == 1) {
-        q[0] = (int8_t)c[0];
-    } else {
-        uint32_t u[N / 4];
+    uint32_t u[N / 4];
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i)
-            u[i] = (c[4 * i] & 255) | (c[4 * i + 1] & 255) << 8 | (c[4 * i + 2] & 255) << 16 | (uint32_t)c[4 * i + 3] << 24;
-        if constexpr (N == 4) {
-            *reinterpret_cast<uint32_t*>(q) = u[0];
-        } else {
-            *reinterpret_cast<uint2*>(q) = make_uint2(u[0], u[1]);
-        }
+    for (int i = 0; i < N / 4; ++i)
+        u[i] = (c[4 * i] & 255) | (c[4 * i + 1] & 255) << 8 | (c[4 * i + 2] & 255) << 16 | (uint32_t)c[4 * i + 3] << 24;
+    if (AL) {
+        __builtin_memcpy(__builtin_assume_aligned(q, N), u, N);
+    } else if (left >= N) {
+        __builtin_memcpy(q, u, N);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (e < left) q[e] = (int8_t)c[e];
     }
 }
 
@@ -153,23 +169,24 @@ __device__ __forceinline__ void zero_unless(bool keep, float (&p)[N]) {
 // One row per workgroup, the row in registers.  NORM: the norm (w of type E,
 // outputs h, y, q, rstd as asked); otherwise rows to 8 bits (w an optional
 // fp32 column scale).
-template <typename E, typename W, int N, int P, bool NORM>
-__global__ __launch_bounds__(P > 2 ? 512 : 1024) void row_regs(RowArgs a) {
+template <typename E, typename W, bool AL, int P, bool NORM>
+__global__ __launch_bounds__(P > 4 ? 512 : 1024) void row_regs(RowArgs a) {
+    constexpr int N = Pack<E>::N;
     __shared__ float rs[kMaxWaves];
     __shared__ uint32_t rt[kMaxWaves];
     const int64_t row = a.row0 + blockIdx.x, off = row * a.d;
     const E* x = static_cast<const E*>(a.x) + off;
     const W* w = static_cast<const W*>(a.w);
-    const int n = (int)(a.d / N), nt = blockDim.x;
+    const int d = (int)a.d, n = (d + N - 1) / N, nt = blockDim.x;
     float v[P][N], p[P][N];
     {
-        Elems<E, N> xv[P], rv[P];
+        Pack<E> xv[P], rv[P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int k = threadIdx.x + i * nt;
             if (k < n) {
-                xv[i].load(x + (int64_t)k * N);
-                if (NORM && a.res) rv[i].load(static_cast<const E*>(a.res) + off + (int64_t)k * N);
+                xv[i] = load_row<E, AL>(x + k * N, d - k * N);
+                if (NORM && a.res) rv[i] = load_row<E, AL>(static_cast<const E*>(a.res) + off + k * N, d - k * N);
             }
         }
 #pragma unroll
@@ -177,8 +194,8 @@ __global__ __launch_bounds__(P > 2 ? 512 : 1024) void row_regs(RowArgs a) {
             const int k = threadIdx.x + i * nt;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                v[i][e] = k < n ? xv[i][e] : 0.0f;
-                if (NORM && a.res) v[i][e] += k < n ? rv[i][e] : 0.0f;
+                v[i][e] = k < n ? at(xv[i], e) : 0.0f;
+                if (NORM && a.res) v[i][e] += k < n ? at(rv[i], e) : 0.0f;
             }
         }
     }
@@ -190,7 +207,7 @@ __global__ __launch_bounds__(P > 2 ? 512 : 1024) void row_regs(RowArgs a) {
         float wv[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) wv[e] = 1.0f;
-        if (k < n && w) load_w<W, N>(w, (int64_t)k * N, wv);
+        if (k < n && w) load_w<W, AL>(w + k * N, d - k * N, wv);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             if (NORM) sum = fmaf(v[i][e], v[i][e], sum);
@@ -198,7 +215,7 @@ __global__ __launch_bounds__(P > 2 ? 512 : 1024) void row_regs(RowArgs a) {
             const uint32_t m = __float_as_uint(p[i][e]) & 0x7fffffffu;
             top = m > top ? m : top;
         }
-        if (NORM && a.h && k < n) store_n<E, N>(static_cast<E*>(a.h) + off + (int64_t)k * N, v[i]);
+        if (NORM && a.h && k < n) store_row<E, AL>(static_cast<E*>(a.h) + off + k * N, v[i], d - k * N);
     }
     block_reduce(sum, top, rs, rt);
     const float rstd = NORM ? 1.0f / sqrtf(sum / (float)a.d + a.eps) : 1.0f;
@@ -216,37 +233,37 @@ __global__ __launch_bounds__(P > 2 ? 512 : 1024) void row_regs(RowArgs a) {
             float yv[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) yv[e] = p[i][e] * rstd;
-            store_n<E, N>(static_cast<E*>(a.y) + off + (int64_t)k * N, yv);
+            store_row<E, AL>(static_cast<E*>(a.y) + off + k * N, yv, d - k * N);
         }
         if (a.q) {
             zero_unless<N>(inv != 0.0f, p[i]);
-            store_codes<N>(a.q + off + (int64_t)k * N, p[i], inv);
+            store_codes<AL>(a.q + off + k * N, p[i], inv, d - k * N);
         }
     }
 }
 
 // The same for rows of any length, read twice.
-template <typename E, typename W, int N, bool NORM>
+template <typename E, typename W, bool AL, bool NORM>
 __global__ __launch_bounds__(1024) void row_long(RowArgs a) {
+    constexpr int N = Pack<E>::N;
     __shared__ float rs[kMaxWaves];
     __shared__ uint32_t rt[kMaxWaves];
-    const int64_t row = a.row0 + blockIdx.x, off = row * a.d, n = a.d / N;
+    const int64_t row = a.row0 + blockIdx.x, off = row * a.d, n = (a.d + N - 1) / N;
     const E* x = static_cast<const E*>(a.x) + off;
     const E* r = NORM && a.res ? static_cast<const E*>(a.res) + off : nullptr;
     const W* w = static_cast<const W*>(a.w);
-    auto at = [&](int64_t k, float (&v)[N], float (&p)[N]) __attribute__((always_inline)) {
-        Elems<E, N> t;
-        t.load(x + k * N);
+    auto pack = [&](int64_t k, float (&v)[N], float (&p)[N]) __attribute__((always_inline)) {
+        Pack<E> t = load_row<E, AL>(x + k * N, a.d - k * N);
 #pragma unroll
-        for (int e = 0; e < N; ++e) v[e] = t[e];
+        for (int e = 0; e < N; ++e) v[e] = at(t, e);
         if (r) {
-            t.load(r + k * N);
+            t = load_row<E, AL>(r + k * N, a.d - k * N);
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] += t[e];
+            for (int e = 0; e < N; ++e) v[e] += at(t, e);
         }
 #pragma unroll
         for (int e = 0; e < N; ++e) p[e] = 1.0f;
-        if (w) load_w<W, N>(w, k * N, p);
+        if (w) load_w<W, AL>(w + k * N, a.d - k * N, p);
 #pragma unroll
         for (int e = 0; e < N; ++e) p[e] *= v[e];
     };
@@ -254,7 +271,7 @@ __global__ __launch_bounds__(1024) void row_long(RowArgs a) {
     uint32_t top = 0;
     for (int64_t k = threadIdx.x; k < n; k += blockDim.x) {
         float v[N], p[N];
-        at(k, v, p);
+        pack(k, v, p);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
             if (NORM) sum = fmaf(v[e], v[e], sum);
@@ -274,17 +291,18 @@ __global__ __launch_bounds__(1024) void row_long(RowArgs a) {
     // residual itself
     for (int64_t k = threadIdx.x; k < n; k += blockDim.x) {
         float v[N], p[N];
-        at(k, v, p);
-        if (NORM && a.h) store_n<E, N>(static_cast<E*>(a.h) + off + k * N, v);
+        pack(k, v, p);
+        const int64_t left = a.d - k * N;
+        if (NORM && a.h) store_row<E, AL>(static_cast<E*>(a.h) + off + k * N, v, left);
         if (NORM && a.y) {
             float yv[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) yv[e] = p[e] * rstd;
-            store_n<E, N>(static_cast<E*>(a.y) + off + k * N, yv);
+            store_row<E, AL>(static_cast<E*>(a.y) + off + k * N, yv, left);
         }
         if (a.q) {
             zero_unless<N>(inv != 0.0f, p);
-            store_codes<N>(a.q + off + k * N, p, inv);
+            store_codes<AL>(a.q + off + k * N, p, inv, left);
         }
     }
 }
@@ -303,32 +321,39 @@ struct BwdArgs {
 };
 
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ... of one workgroup, each in
-// registers between its reduction and its store.
-template <typename E, int N, int P>
-__global__ __launch_bounds__(P > 2 ? 512 : 1024) void rms_bwd_regs(BwdArgs a) {
+// registers between its reduction and its store.  Six accesses a thread, for
+// the longest rows, leave no registers for w and dh: they are loaded where
+// they are used (registers that spill cost more: 60 us instead of 18 at 2048
+// x 5120 when 4 accesses were held to 128).
+template <typename E, bool AL, int P>
+__global__ __launch_bounds__(P < 4 ? 1024 : P == 4 ? 512 : 640) void rms_bwd_regs(BwdArgs a) {
+    constexpr int N = Pack<E>::N;
+    constexpr bool WIDE = P > 4;
     __shared__ float rs[2][kMaxWaves];
     __shared__ uint32_t rt[2][kMaxWaves];
-    const int n = (int)(a.d / N), nt = blockDim.x;
-    Elems<E, N> wv[P];
+    const int d = (int)a.d, n = (d + N - 1) / N, nt = blockDim.x;
+    const E* w = static_cast<const E*>(a.w);
+    Pack<E> wv[WIDE ? 1 : P];
     float dw[P][N];
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int k = threadIdx.x + i * nt;
 #pragma unroll
         for (int e = 0; e < N; ++e) dw[i][e] = 0.0f;
-        if (k < n) wv[i].load(static_cast<const E*>(a.w) + (int64_t)k * N);
+        if (!WIDE && k < n) wv[i] = load_row<E, AL>(w + k * N, d - k * N);
     }
     int par = 0;   // the reduction's buffer: the other one than the last row's, which slow waves may still read
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x, par ^= 1) {
         const int64_t off = row * a.d;
-        Elems<E, N> dyv[P], hv[P], gv[P];
+        const E* dh = a.dh ? static_cast<const E*>(a.dh) + off : nullptr;
+        Pack<E> dyv[P], hv[P], gv[WIDE ? 1 : P];
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int k = threadIdx.x + i * nt;
             if (k < n) {
-                dyv[i].load(static_cast<const E*>(a.dy) + off + (int64_t)k * N);
-                hv[i].load(static_cast<const E*>(a.h) + off + (int64_t)k * N);
-                if (a.dh) gv[i].load(static_cast<const E*>(a.dh) + off + (int64_t)k * N);
+                dyv[i] = load_row<E, AL>(static_cast<const E*>(a.dy) + off + k * N, d - k * N);
+                hv[i] = load_row<E, AL>(static_cast<const E*>(a.h) + off + k * N, d - k * N);
+                if (!WIDE && dh) gv[i] = load_row<E, AL>(dh + k * N, d - k * N);
             }
         }
         const float r = a.rstd[row];
@@ -336,11 +361,13 @@ __global__ __launch_bounds__(P > 2 ? 512 : 1024) void rms_bwd_regs(BwdArgs a) {
         uint32_t none = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            if (threadIdx.x + i * nt >= n) continue;
+            const int k = threadIdx.x + i * nt;
+            if (k >= n) continue;
+            if (WIDE) wv[0] = load_row<E, AL>(w + k * N, d - k * N);
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float dv = dyv[i][e], hh = hv[i][e];
-                c = fmaf(dv * wv[i][e], hh, c);
+                const float dv = at(dyv[i], e), hh = at(hv[i], e);
+                c = fmaf(dv * at(wv[WIDE ? 0 : i], e), hh, c);
                 dw[i][e] = fmaf(dv, hh * r, dw[i][e]);
             }
         }
@@ -348,15 +375,22 @@ __global__ __launch_bounds__(P > 2 ? 512 : 1024) void rms_bwd_regs(BwdArgs a) {
         const float f = c / (float)a.d * r * r;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
+            // the row is kept as it was loaded: without this the compiler
+            // holds the fp32 values of the first use, twice the registers
+            asm volatile("" : "+v"(dyv[i].u), "+v"(hv[i].u));
             const int k = threadIdx.x + i * nt;
             if (k >= n) continue;
+            if (WIDE) {
+                wv[0] = load_row<E, AL>(w + k * N, d - k * N);
+                if (dh) gv[0] = load_row<E, AL>(dh + k * N, d - k * N);
+            }
             float o[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float u = dyv[i][e] * wv[i][e];
-                o[e] = r * (u - hv[i][e] * f) + (a.dh ? gv[i][e] : 0.0f);
+                const float u = at(dyv[i], e) * at(wv[WIDE ? 0 : i], e);
+                o[e] = r * (u - at(hv[i], e) * f) + (dh ? at(gv[WIDE ? 0 : i], e) : 0.0f);
             }
-            store_n<E, N>(static_cast<E*>(a.dx) + off + (int64_t)k * N, o);
+            store_row<E, AL>(static_cast<E*>(a.dx) + off + k * N, o, d - k * N);
         }
     }
     if (a.part) {
@@ -364,9 +398,10 @@ __global__ __launch_bounds__(P > 2 ? 512 : 1024) void rms_bwd_regs(BwdArgs a) {
         for (int i = 0; i < P; ++i) {
             const int k = threadIdx.x + i * nt;
             if (k >= n) continue;
-            float* dst = a.part + (int64_t)blockIdx.x * a.d + (int64_t)k * N;
+            float* dst = a.part + (int64_t)blockIdx.x * a.d + k * N;
 #pragma unroll
-            for (int e = 0; e < N; ++e) dst[e] = dw[i][e];
+            for (int e = 0; e < N; ++e)
+                if (AL || k * N + e < d) dst[e] = dw[i][e];
         }
     }
 }
@@ -409,25 +444,52 @@ __global__ __launch_bounds__(256) void rms_dw_cols(BwdArgs a) {
 }
 
 // dw_j = sum of the partials of column j: lane w of a column adds partials w,
-// w + 8, ... in order, then the eight sums in order.
-constexpr int kDwCols = 32, kDwLanes = 8;
+// w + kDwLanes, ... in order, a batch of loads at a time, then the lanes' sums
+// are added in order.  N columns a thread (16 bytes where d is a multiple of
+// 4).  One load at a time took 20 us at 512 x 5120, more than the pass before
+// it.
+constexpr int kDwCols = 32, kDwBatch = 16;
 
+template <int N>
 __global__ __launch_bounds__(256) void dw_finalize(const float* __restrict__ part, int nparts, int64_t d,
                                                    float* __restrict__ dw) {
+    constexpr int kThreads = kDwCols / N, kDwLanes = 256 / kThreads;
     __shared__ float red[kDwLanes][kDwCols];
-    const int c = threadIdx.x % kDwCols, w = threadIdx.x / kDwCols;
+    const int c = threadIdx.x % kThreads * N, w = threadIdx.x / kThreads;
     for (int64_t j0 = (int64_t)blockIdx.x * kDwCols; j0 < d; j0 += (int64_t)gridDim.x * kDwCols) {
         const int64_t j = j0 + c;
-        float s = 0.0f;
-        if (j < d)
-            for (int p = w; p < nparts; p += kDwLanes) s += part[(int64_t)p * d + j];
-        red[w][c] = s;
-        __syncthreads();
-        if (w == 0 && j < d) {
-            float v = red[0][c];
+        float s[N];
 #pragma unroll
-            for (int q = 1; q < kDwLanes; ++q) v += red[q][c];
-            dw[j] = v;
+        for (int e = 0; e < N; ++e) s[e] = 0.0f;
+        if (j < d) {
+            for (int p0 = w; p0 < nparts; p0 += kDwLanes * kDwBatch) {
+                float v[kDwBatch][N];
+#pragma unroll
+                for (int i = 0; i < kDwBatch; ++i) {
+                    const int p = p0 + i * kDwLanes;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) v[i][e] = 0.0f;
+                    if (p >= nparts) continue;
+                    if constexpr (N == 1)
+                        v[i][0] = part[(int64_t)p * d + j];
+                    else
+                        load_w<float, true>(part + (int64_t)p * d + j, N, v[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < kDwBatch; ++i)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) s[e] += v[i][e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < N; ++e) red[w][c + e] = s[e];
+        __syncthreads();
+        const int64_t o = j0 + threadIdx.x;
+        if (threadIdx.x < kDwCols && o < d) {
+            float v = red[0][threadIdx.x];
+#pragma unroll
+            for (int q = 1; q < kDwLanes; ++q) v += red[q][threadIdx.x];
+            dw[o] = v;
         }
         __syncthreads();
     }
@@ -435,19 +497,30 @@ __global__ __launch_bounds__(256) void dw_finalize(const float* __restrict__ par
 
 // ------------------------------------------------------------- dequantise
 
-template <typename E, int N>
+template <typename E, bool AL>
 __global__ __launch_bounds__(256) void dequantize(const int8_t* __restrict__ q, const float* __restrict__ scale,
                                                   int64_t rows, int64_t d, E* __restrict__ out) {
+    constexpr int N = Pack<E>::N;
+    const int64_t n = (d + N - 1) / N;
     for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
         const float s = scale[row];
-        for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < d / N; k += (int64_t)gridDim.x * 256) {
-            float v[N];
+        for (int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x; k < n; k += (int64_t)gridDim.x * 256) {
             const int8_t* src = q + row * d + k * N;
-            int8_t c[N];
-            __builtin_memcpy(c, N == 1 ? src : static_cast<const int8_t*>(__builtin_assume_aligned(src, N)), N);
+            const int64_t left = d - k * N;
+            int8_t c[N] = {};
+            if (AL) {
+                __builtin_memcpy(c, __builtin_assume_aligned(src, N), N);
+            } else if (left >= N) {
+                __builtin_memcpy(c, src, N);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (e < left) c[e] = src[e];
+            }
+            float v[N];
 #pragma unroll
             for (int e = 0; e < N; ++e) v[e] = (float)c[e] * s;
-            store_n<E, N>(out + row * d + k * N, v);
+            store_row<E, AL>(out + row * d + k * N, v, left);
         }
     }
 }
@@ -465,33 +538,32 @@ struct RowShape {
     int p, nt;
 };
 
-RowShape row_shape(int64_t n, int64_t rows) {
+// Up to 4 accesses a thread a workgroup may have 1024 threads, with 8 of them
+// 512 (pmax: the most that a kernel is built for).
+RowShape row_shape(int64_t n, int64_t rows, int pmax) {
     const int64_t most = rows >= kManyRows ? 256 : 1024;
     int p = 1;
-    while (p < 8 && n > most * p) p *= 2;
+    while (p < pmax && n > most * p) p *= 2;
     const int64_t nt = ((n + p - 1) / p + 63) / 64 * 64;
-    if (nt > (p > 2 ? 512 : 1024)) {
-        if (n > 8 * 512) return {0, 1024};
-        return {8, (int)(((n + 7) / 8 + 63) / 64 * 64)};
-    }
+    if (nt > (p > 4 ? 512 : 1024)) return {0, 1024};
     return {p, (int)nt};
 }
 
 // Rows per launch: a grid's threads are counted in 32 bits.
 constexpr int64_t kRowsPerLaunch = (int64_t)1 << 21;
 
-template <typename E, typename W, int N, bool NORM>
+template <typename E, typename W, bool AL, bool NORM>
 hipError_t launch_rows(RowArgs a, hipStream_t st) {
-    const RowShape s = row_shape(a.d / N, a.rows);
+    const RowShape s = row_shape((a.d + Pack<E>::N - 1) / Pack<E>::N, a.rows, 8);
     for (a.row0 = 0; a.row0 < a.rows; a.row0 += kRowsPerLaunch) {
         const int64_t left = a.rows - a.row0;
         const unsigned g = (unsigned)(left < kRowsPerLaunch ? left : kRowsPerLaunch);
         switch (s.p) {
-            case 1: row_regs<E, W, N, 1, NORM><<<g, s.nt, 0, st>>>(a); break;
-            case 2: row_regs<E, W, N, 2, NORM><<<g, s.nt, 0, st>>>(a); break;
-            case 4: row_regs<E, W, N, 4, NORM><<<g, s.nt, 0, st>>>(a); break;
-            case 8: row_regs<E, W, N, 8, NORM><<<g, s.nt, 0, st>>>(a); break;
-            default: row_long<E, W, N, NORM><<<g, s.nt, 0, st>>>(a); break;
+            case 1: row_regs<E, W, AL, 1, NORM><<<g, s.nt, 0, st>>>(a); break;
+            case 2: row_regs<E, W, AL, 2, NORM><<<g, s.nt, 0, st>>>(a); break;
+            case 4: row_regs<E, W, AL, 4, NORM><<<g, s.nt, 0, st>>>(a); break;
+            case 8: row_regs<E, W, AL, 8, NORM><<<g, s.nt, 0, st>>>(a); break;
+            default: row_long<E, W, AL, NORM><<<g, s.nt, 0, st>>>(a); break;
         }
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -504,30 +576,37 @@ hipError_t norm_typed(const RowArgs& a, hipStream_t st) {
     constexpr int N = Pack<E>::N;
     const bool vec = a.d % N == 0 && aligned_to(a.x, 16) && aligned_to(a.res, 16) && aligned_to(a.w, 16) &&
                      aligned_to(a.h, 16) && aligned_to(a.y, 16) && aligned_to(a.q, N);
-    return vec ? launch_rows<E, E, N, true>(a, st) : launch_rows<E, E, 1, true>(a, st);
+    return vec ? launch_rows<E, E, true, true>(a, st) : launch_rows<E, E, false, true>(a, st);
 }
 
 template <typename E>
 hipError_t quantize_typed(const RowArgs& a, hipStream_t st) {
     constexpr int N = Pack<E>::N;
     const bool vec = a.d % N == 0 && aligned_to(a.x, 16) && aligned_to(a.w, 16) && aligned_to(a.q, N);
-    return vec ? launch_rows<E, float, N, false>(a, st) : launch_rows<E, float, 1, false>(a, st);
+    return vec ? launch_rows<E, float, true, false>(a, st) : launch_rows<E, float, false, false>(a, st);
 }
 
-// Workgroups of the backward pass, each with its own row of dw partials.
-constexpr int kBwdParts = 512;
+// Workgroups of the backward pass, each with its own row of dw partials: one
+// for each row up to a CU each, then four rows each, so that the partials stay
+// a fraction of what is read.
+constexpr int64_t kBwdParts = 512, kBwdRows = 4;
 
-int bwd_parts(int64_t rows) { return (int)(rows < kBwdParts ? rows : kBwdParts); }
+int bwd_parts(int64_t rows) {
+    if (rows <= 256) return (int)rows;
+    const int64_t p = (rows + kBwdRows - 1) / kBwdRows;
+    return (int)(p < 256 ? 256 : p < kBwdParts ? p : kBwdParts);
+}
 
-template <typename E, int N>
+template <typename E, bool AL>
 bool launch_bwd_regs(const BwdArgs& a, int parts, hipStream_t st) {
-    const RowShape s = row_shape(a.d / N, a.rows);
+    const int64_t n = (a.d + Pack<E>::N - 1) / Pack<E>::N;
+    const RowShape s = n <= 4 * 512 ? row_shape(n, a.rows, 4) : RowShape{6, (int)(((n + 5) / 6 + 63) / 64 * 64)};
+    if (n > 6 * 640) return false;
     switch (s.p) {
-        case 1: rms_bwd_regs<E, N, 1><<<parts, s.nt, 0, st>>>(a); break;
-        case 2: rms_bwd_regs<E, N, 2><<<parts, s.nt, 0, st>>>(a); break;
-        case 4: rms_bwd_regs<E, N, 4><<<parts, s.nt, 0, st>>>(a); break;
-        case 8: rms_bwd_regs<E, N, 8><<<parts, s.nt, 0, st>>>(a); break;
-        default: return false;
+        case 1: rms_bwd_regs<E, AL, 1><<<parts, s.nt, 0, st>>>(a); break;
+        case 2: rms_bwd_regs<E, AL, 2><<<parts, s.nt, 0, st>>>(a); break;
+        case 4: rms_bwd_regs<E, AL, 4><<<parts, s.nt, 0, st>>>(a); break;
+        default: rms_bwd_regs<E, AL, 6><<<parts, s.nt, 0, st>>>(a); break;
     }
     return true;
 }
@@ -539,7 +618,7 @@ hipError_t bwd_typed(BwdArgs a, float* dw, hipStream_t st) {
     if (a.rows > 0) {
         const bool vec = a.d % N == 0 && aligned_to(a.dy, 16) && aligned_to(a.h, 16) && aligned_to(a.w, 16) &&
                          aligned_to(a.dh, 16) && aligned_to(a.dx, 16);
-        if (!(vec ? launch_bwd_regs<E, N>(a, parts, st) : launch_bwd_regs<E, 1>(a, parts, st))) {
+        if (!(vec ? launch_bwd_regs<E, true>(a, parts, st) : launch_bwd_regs<E, false>(a, parts, st))) {
             // the columns first: dx may be written over dy or dh
             if (a.part) {
                 rms_dw_cols<E><<<dim3((unsigned)((a.d + 255) / 256), (unsigned)parts), 256, 0, st>>>(a);
@@ -558,7 +637,12 @@ hipError_t bwd_typed(BwdArgs a, float* dw, hipStream_t st) {
     }
     if (dw) {
         const int64_t g = (a.d + kDwCols - 1) / kDwCols;
-        dw_finalize<<<(unsigned)(g < 65536 ? g : 65536), 256, 0, st>>>(a.part, a.rows > 0 ? parts : 0, a.d, dw);
+        const unsigned grid = (unsigned)(g < 65536 ? g : 65536);
+        const int n = a.rows > 0 ? parts : 0;
+        if (a.d % 4 == 0)   // the workspace is 256-byte aligned
+            dw_finalize<4><<<grid, 256, 0, st>>>(a.part, n, a.d, dw);
+        else
+            dw_finalize<1><<<grid, 256, 0, st>>>(a.part, n, a.d, dw);
     }
     return hipGetLastError();
 }
@@ -567,14 +651,13 @@ template <typename E>
 hipError_t dequantize_typed(const int8_t* q, const float* scale, int64_t rows, int64_t d, void* out, hipStream_t st) {
     constexpr int N = Pack<E>::N;
     const bool vec = d % N == 0 && aligned_to(q, N) && aligned_to(out, 16);
-    const int64_t n = vec ? d / N : d;
-    int64_t gx = (n + 255) / 256;
+    int64_t gx = ((d + N - 1) / N + 255) / 256;
     if (gx > 64) gx = 64;
     const dim3 grid((unsigned)gx, (unsigned)(rows < 65535 ? rows : 65535));
     if (vec)
-        dequantize<E, N><<<grid, 256, 0, st>>>(q, scale, rows, d, static_cast<E*>(out));
+        dequantize<E, true><<<grid, 256, 0, st>>>(q, scale, rows, d, static_cast<E*>(out));
     else
-        dequantize<E, 1><<<grid, 256, 0, st>>>(q, scale, rows, d, static_cast<E*>(out));
+        dequantize<E, false><<<grid, 256, 0, st>>>(q, scale, rows, d, static_cast<E*>(out));
     return hipGetLastError();
 }
 

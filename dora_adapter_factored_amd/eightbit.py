@@ -9,56 +9,100 @@ activation in 8 bits is the same with a scale per token.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
-from .binding import _DTYPE_CODE, _check, _need, _ptr, _stream, load, workspace
+from .binding import _DTYPE_CODE, _check, _need, _ws_cache, load, workspace
 
 _F32, _I8 = torch.float32, torch.int8
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+# A decoding step's calls take a few microseconds on the GPU, no more than the
+# host spends on one: arguments are compared in place, and pointers and the
+# stream are passed as plain integers.
 
 
-def _rows(t, name: str):
-    """(device, dtype, rows, row length) of a contiguous 2-D float tensor."""
+def _stream(device) -> int:
+    """The current stream's handle (torch.cuda.current_stream builds an object for it)."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU (got {device})")
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
+def _matrix(t, name: str):
+    """(device, dtype, shape) of a contiguous 2-D float tensor."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != 2:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} has shape {tuple(shape)}, expected two dimensions")
     if t.dtype not in _DTYPE_CODE:
         raise ValueError(f"unsupported dtype {t.dtype} of {name}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    return t.device, t.dtype, t.shape[0], t.shape[1]
+    return t.device, t.dtype, shape
 
 
-def _out(t, name: str, device, dtype, shape):
+def _in(t, name: str, device, dtype, shape) -> int:
+    """The pointer of an argument that has to be this; _need says what it is not."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or t.device != device or \
+            not t.is_contiguous():
+        _need(t, name, device, dtype, shape)
+    return t.data_ptr()
+
+
+def _out(t, name: str, device, dtype, shape, like=None):
+    """An output: the caller's, or a new one (like another tensor where there is one of its kind: that is quicker)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _need(t, name, device, dtype, shape)
+        return torch.empty(shape, dtype=dtype, device=device) if like is None else torch.empty_like(like)
+    _in(t, name, device, dtype, shape)
     return t
 
 
-def _nbytes(ws) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
-
-
+@functools.lru_cache(maxsize=4096)
 def rmsnorm_backward_workspace_size(T: int, d: int) -> int:
     n = ctypes.c_size_t(0)
     _check(load().dora_rmsnorm_backward_workspace_size(T, d, ctypes.byref(n)), "dora_rmsnorm_backward_workspace_size")
     return n.value
 
 
+@functools.lru_cache(maxsize=4096)
 def matmul_q8_workspace_size(T: int, d_out: int, d_in: int) -> int:
     n = ctypes.c_size_t(0)
     _check(load().dora_matmul_q8_workspace_size(T, d_out, d_in, ctypes.byref(n)), "dora_matmul_q8_workspace_size")
     return n.value
 
 
+def _scratch(nbytes: int, ws, device):
+    """(pointer, bytes) of the caller's workspace, or of the cached one of this stream."""
+    if ws is None:
+        if nbytes == 0:
+            return None, 0
+        ws = _ws_cache.get((device, _stream(device)))   # workspace()'s own key
+        if ws is None or ws.numel() < nbytes:
+            ws = workspace(nbytes, device)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 # ------------------------------------------------------------ norm
-def _norm(x, w, eps, residual, h, y, q, scale, rstd):
-    dev, dt, T, d = _rows(x, "x")
-    _need(w, "w", dev, dt, (d,))
-    _check(load().dora_rmsnorm(_ptr(x), _ptr(residual), _ptr(w), float(eps), T, d, _DTYPE_CODE[dt], _ptr(h), _ptr(y),
-                               _ptr(q), _ptr(scale), _ptr(rstd), _stream(dev)), "dora_rmsnorm")
+def _norm(x, w, eps, residual, h, dev, dt, shape, y, q, scale, rstd):
+    """The call, and h: x itself where there is no residual."""
+    wp = _in(w, "w", dev, dt, shape[1:])
+    rp = hp = None
+    if residual is not None:
+        rp = _in(residual, "residual", dev, dt, shape)
+        h = _out(h, "h", dev, dt, shape, x)
+        hp = h.data_ptr()
+    elif h is not None:
+        raise ValueError("h is an output of the addition: it needs a residual")
+    st = load().dora_rmsnorm(x.data_ptr(), rp, wp, eps, shape[0], shape[1], _DTYPE_CODE[dt], hp,
+                             None if y is None else y.data_ptr(), None if q is None else q.data_ptr(),
+                             None if scale is None else scale.data_ptr(), None if rstd is None else rstd.data_ptr(),
+                             _stream(dev))
+    if st:
+        _check(st, "dora_rmsnorm")
+    return x if residual is None else h
 
 
 def rmsnorm(x, w, eps: float, residual=None, *, y=None, h=None, rstd=None):
@@ -67,16 +111,11 @@ def rmsnorm(x, w, eps: float, residual=None, *, y=None, h=None, rstd=None):
     x, residual [T, d] and w [d] share a dtype (fp32, bf16 or fp16).  Without a
     residual h is x itself.  h=x or h=residual adds in place.
     """
-    dev, dt, T, d = _rows(x, "x")
-    y = _out(y, "y", dev, dt, (T, d))
-    rstd = _out(rstd, "rstd", dev, _F32, (T,))
-    if residual is not None:
-        _need(residual, "residual", dev, dt, (T, d))
-        h = _out(h, "h", dev, dt, (T, d))
-    elif h is not None:
-        raise ValueError("h is an output of the addition: it needs a residual")
-    _norm(x, w, eps, residual, h, y, None, None, rstd)
-    return y, (x if residual is None else h), rstd
+    dev, dt, shape = _matrix(x, "x")
+    y = _out(y, "y", dev, dt, shape, x)
+    rstd = _out(rstd, "rstd", dev, _F32, shape[:1])
+    h = _norm(x, w, eps, residual, h, dev, dt, shape, y, None, None, rstd)
+    return y, h, rstd
 
 
 def rmsnorm_q8(x, w, eps: float, residual=None, *, q=None, scale=None, h=None, y=None):
@@ -85,70 +124,76 @@ def rmsnorm_q8(x, w, eps: float, residual=None, *, q=None, scale=None, h=None, y
     As rmsnorm, with y quantised before it is rounded.  y=tensor [T, d] also
     writes y itself (an unmerged adapter's branch reads it).
     """
-    dev, dt, T, d = _rows(x, "x")
-    q = _out(q, "q", dev, _I8, (T, d))
-    scale = _out(scale, "scale", dev, _F32, (T,))
+    dev, dt, shape = _matrix(x, "x")
+    q = _out(q, "q", dev, _I8, shape)
+    scale = _out(scale, "scale", dev, _F32, shape[:1])
     if y is not None:
-        _need(y, "y", dev, dt, (T, d))
-    if residual is not None:
-        _need(residual, "residual", dev, dt, (T, d))
-        h = _out(h, "h", dev, dt, (T, d))
-    elif h is not None:
-        raise ValueError("h is an output of the addition: it needs a residual")
-    _norm(x, w, eps, residual, h, y, q, scale, None)
-    return q, scale, (x if residual is None else h)
+        _in(y, "y", dev, dt, shape)
+    h = _norm(x, w, eps, residual, h, dev, dt, shape, y, q, scale, None)
+    return q, scale, h
 
 
 def rmsnorm_backward(dy, h, w, rstd, dh=None, *, need_dw: bool = True, dx=None, dw=None, ws=None):
     """(dx, dw) of rmsnorm's y (gradient dy) and h (gradient dh or None); dx is the
     gradient of x and of the residual, dw is fp32 [d] (None unless need_dw)."""
-    dev, dt, T, d = _rows(dy, "dy")
-    _need(h, "h", dev, dt, (T, d))
-    _need(w, "w", dev, dt, (d,))
-    _need(rstd, "rstd", dev, _F32, (T,))
-    if dh is not None:
-        _need(dh, "dh", dev, dt, (T, d))
-    dx = _out(dx, "dx", dev, dt, (T, d))
+    dev, dt, shape = _matrix(dy, "dy")
+    T, d = shape
+    hp = _in(h, "h", dev, dt, shape)
+    wp = _in(w, "w", dev, dt, shape[1:])
+    rp = _in(rstd, "rstd", dev, _F32, shape[:1])
+    dhp = None if dh is None else _in(dh, "dh", dev, dt, shape)
+    dx = _out(dx, "dx", dev, dt, shape, dy)
     if need_dw:
-        dw = _out(dw, "dw", dev, _F32, (d,))
-        if ws is None:
-            ws = workspace(rmsnorm_backward_workspace_size(T, d), dev)
-    _check(load().dora_rmsnorm_backward(_ptr(dy), _ptr(h), _ptr(w), _ptr(rstd), _ptr(dh), T, d, _DTYPE_CODE[dt],
-                                        _ptr(dx), _ptr(dw) if need_dw else None, _ptr(ws), _nbytes(ws), _stream(dev)),
-           "dora_rmsnorm_backward")
-    return dx, (dw if need_dw else None)
+        dw = _out(dw, "dw", dev, _F32, shape[1:])
+        wsp, nbytes = _scratch(rmsnorm_backward_workspace_size(T, d), ws, dev)
+    else:
+        dw, wsp, nbytes = None, None, 0
+    st = load().dora_rmsnorm_backward(dy.data_ptr(), hp, wp, rp, dhp, T, d, _DTYPE_CODE[dt], dx.data_ptr(),
+                                      None if dw is None else dw.data_ptr(), wsp, nbytes, _stream(dev))
+    if st:
+        _check(st, "dora_rmsnorm_backward")
+    return dx, dw
 
 
 # ------------------------------------------------------------ rows in 8 bits
 def quantize_rows(x, col_scale=None, *, q=None, scale=None):
     """(q, scale): the rows of x * col_scale as int8 codes in [-127, 127] with an fp32 scale each."""
-    dev, dt, n, d = _rows(x, "x")
-    if col_scale is not None:
-        _need(col_scale, "col_scale", dev, _F32, (d,))
-    q = _out(q, "q", dev, _I8, (n, d))
-    scale = _out(scale, "scale", dev, _F32, (n,))
-    _check(load().dora_quantize_rows(_ptr(x), _ptr(col_scale), n, d, _DTYPE_CODE[dt], _ptr(q), _ptr(scale),
-                                     _stream(dev)), "dora_quantize_rows")
+    dev, dt, shape = _matrix(x, "x")
+    cp = None if col_scale is None else _in(col_scale, "col_scale", dev, _F32, shape[1:])
+    q = _out(q, "q", dev, _I8, shape)
+    scale = _out(scale, "scale", dev, _F32, shape[:1])
+    st = load().dora_quantize_rows(x.data_ptr(), cp, shape[0], shape[1], _DTYPE_CODE[dt], q.data_ptr(),
+                                   scale.data_ptr(), _stream(dev))
+    if st:
+        _check(st, "dora_quantize_rows")
     return q, scale
 
 
 def dequantize_rows(q, scale, dtype: torch.dtype, *, out=None):
     """q * scale by rows, rounded once to dtype."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 2:
-        raise ValueError("q must be a torch.Tensor of two dimensions")
+    dev, shape = _codes(q, "q")
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
-    dev = q.device
-    n, d = q.shape
-    _need(q, "q", dev, _I8)
-    _need(scale, "scale", dev, _F32, (n,))
-    out = _out(out, "out", dev, dtype, (n, d))
-    _check(load().dora_dequantize_rows(_ptr(q), _ptr(scale), n, d, _DTYPE_CODE[dtype], _ptr(out), _stream(dev)),
-           "dora_dequantize_rows")
+    sp = _in(scale, "scale", dev, _F32, shape[:1])
+    out = _out(out, "out", dev, dtype, shape)
+    st = load().dora_dequantize_rows(q.data_ptr(), sp, shape[0], shape[1], _DTYPE_CODE[dtype], out.data_ptr(),
+                                     _stream(dev))
+    if st:
+        _check(st, "dora_dequantize_rows")
     return out
 
 
 # ------------------------------------------------------------ product
+def _codes(t, name: str):
+    """(device, shape) of a contiguous 2-D int8 tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if len(shape) != 2 or t.dtype != _I8 or not t.is_contiguous():
+        raise ValueError(f"{name} must be int8, of two dimensions and contiguous (got {t.dtype}, {tuple(shape)})")
+    return t.device, shape
+
+
 def matmul_q8(xq, xscale, wq, wscale=None, dtype: torch.dtype = torch.bfloat16, *, bias=None, g=None, lora_out=None,
               s: float = 1.0, out=None, ws=None):
     """y = base + ((g-1) base + (g s) lora_out) + bias, base = xscale wscale (xq wq^T) with the sum exact.
@@ -157,32 +202,26 @@ def matmul_q8(xq, xscale, wq, wscale=None, dtype: torch.dtype = torch.bfloat16, 
     fp32 [d_out] (None: ones).  g fp32 [d_out] with lora_out [T, d_out] of
     dtype, and bias fp32 [d_out], are optional.  y has dtype.
     """
-    for t, name in ((xq, "xq"), (wq, "wq")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 2:
-            raise ValueError(f"{name} must be a torch.Tensor of two dimensions")
+    dev, (T, K) = _codes(xq, "xq")
+    N = _codes(wq, "wq")[1][0]
+    wp = _in(wq, "wq", dev, _I8, (N, K))
     if dtype not in _DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
-    dev = xq.device
-    T, K = xq.shape
-    N = wq.shape[0]
-    _need(xq, "xq", dev, _I8)
-    _need(wq, "wq", dev, _I8, (N, K))
-    _need(xscale, "xscale", dev, _F32, (T,))
-    if wscale is not None:
-        _need(wscale, "wscale", dev, _F32, (N,))
-    if bias is not None:
-        _need(bias, "bias", dev, _F32, (N,))
     if (g is None) != (lora_out is None):
         raise ValueError("g and lora_out are given together or not at all")
+    xsp = _in(xscale, "xscale", dev, _F32, (T,))
+    wsp = None if wscale is None else _in(wscale, "wscale", dev, _F32, (N,))
+    bp = None if bias is None else _in(bias, "bias", dev, _F32, (N,))
+    gp = lp = None
     if g is not None:
-        _need(g, "g", dev, _F32, (N,))
-        _need(lora_out, "lora_out", dev, dtype, (T, N))
+        gp = _in(g, "g", dev, _F32, (N,))
+        lp = _in(lora_out, "lora_out", dev, dtype, (T, N))
     out = _out(out, "out", dev, dtype, (T, N))
-    if ws is None:
-        ws = workspace(matmul_q8_workspace_size(T, N, K), dev)
-    _check(load().dora_matmul_q8(_ptr(xq), _ptr(xscale), _ptr(wq), _ptr(wscale), _ptr(bias), _ptr(g), _ptr(lora_out),
-                                 float(s), T, N, K, _DTYPE_CODE[dtype], _ptr(out), _ptr(ws), _nbytes(ws),
-                                 _stream(dev)), "dora_matmul_q8")
+    wkp, nbytes = _scratch(matmul_q8_workspace_size(T, N, K), ws, dev)
+    st = load().dora_matmul_q8(xq.data_ptr(), xsp, wp, wsp, bp, gp, lp, s, T, N, K, _DTYPE_CODE[dtype],
+                               out.data_ptr(), wkp, nbytes, _stream(dev))
+    if st:
+        _check(st, "dora_matmul_q8")
     return out
 
 

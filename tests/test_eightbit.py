@@ -178,8 +178,8 @@ def test_empty_calls():
     assert y.shape == (0, 64) and dx.shape == (0, 64) and torch.all(dw == 0) and out.shape == (0, 8)
 
 
-BWD_SHAPES = [(1, 1), (1, 4096), (3, 7), (17, 1003), (600, 512), (1100, 2048), (515, 8200), (2, 28672), (3, 4099),
-              (530, 4200), (3, 66000)]
+BWD_SHAPES = [(1, 1), (1, 4096), (3, 7), (17, 1003), (300, 65), (600, 512), (1100, 2048), (515, 8200), (2, 28672),
+              (3, 4099), (530, 4201), (520, 9001), (3, 30721), (3, 66000)]
 
 
 @pytest.mark.parametrize("T,d", BWD_SHAPES)
@@ -295,10 +295,10 @@ def test_quantize_ties_go_to_even():
 
 
 # ------------------------------------------------------------------ product
-def check_product(T, N, K, dt, adapter=False, bias=False, scaled=True, seed=0, lo=-127, hi=127):
+def check_product(T, N, K, dt, adapter=False, bias=False, scaled=True, seed=0, reference=True):
     g = rng(seed + T * 7 + N * 3 + K)
-    xq = torch.randint(lo, hi + 1, (T, K), generator=g, device=DEV, dtype=torch.int8)
-    wq = torch.randint(lo, hi + 1, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    xq = torch.randint(-127, 128, (T, K), generator=g, device=DEV, dtype=torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
     xs = torch.rand(T, generator=g, device=DEV) * 0.01 + 1e-3
     ws = torch.rand(N, generator=g, device=DEV) * 0.01 + 1e-3 if scaled else None
     if not scaled:
@@ -309,6 +309,8 @@ def check_product(T, N, K, dt, adapter=False, bias=False, scaled=True, seed=0, l
     s = 1.7 if adapter else 1.0
     y = D.matmul_q8(xq, xs, wq, ws, DT[dt], bias=b, g=gg, lora_out=lora, s=s)
     torch.cuda.synchronize()
+    if not reference:
+        return y, (xq, xs, wq, ws, gg, lora, b, s)
     h = lambda t: None if t is None else host64(t)  # noqa: E731
     s32 = float(np.float32(s))
     ref, size = O8.matmul_q8(xq.cpu().numpy(), h(xs), wq.cpu().numpy(), h(ws), h(b), h(gg), h(lora), s32)
@@ -330,6 +332,37 @@ def test_matmul_q8_sizes(T, N, K):
     say(f"[matmul_q8] {T}x{N}x{K}")
     check_product(T, N, K, "bf16")
     check_product(T, N, K, "f32", adapter=True, bias=True)
+
+
+# sizes whose least cost each of the tile forms has, alone and in parts of K
+# (the reference sums on the GPU in fp64, where every sum is exact)
+FORM_SIZES = [
+    # 256 x 256, 192 x 256, 128 x 256, 128 x 128, 64 x 128, 64 x 64 in one part
+    (1814, 6529, 36), (2048, 8192, 384), (900, 8847, 36), (1030, 8200, 264), (523, 7234, 100), (520, 8200, 264),
+    (1753, 1225, 36), (300, 7000, 2000), (65, 8740, 40), (200, 512, 1028), (74, 631, 68),
+    # and in parts
+    (441, 5414, 8276), (134, 5554, 6244), (260, 3780, 5092), (70, 3273, 5676), (513, 2050, 8200), (75, 2113, 4332),
+    (65, 884, 2064), (48, 512, 4100),
+    # rows that are not 4-byte aligned: 64 x 64 and 128 x 128 through registers
+    (200, 900, 2049), (100, 129, 131), (2000, 1300, 1301), (1900, 2051, 130),
+]
+
+
+@pytest.mark.parametrize("T,N,K", FORM_SIZES)
+def test_matmul_q8_forms(T, N, K):
+    say(f"[matmul_q8 forms] {T}x{N}x{K}")
+    for dt, adapter, bias in (("bf16", False, True), ("f32", True, False)):
+        y, (xq, xs, wq, ws, g, lora, b, s) = check_product(T, N, K, dt, adapter, bias, reference=False)
+        base = ((xq.double() @ wq.double().t()) * xs.double()[:, None]) * ws.double()
+        ref, size = base.clone(), base.abs()
+        if adapter:
+            extra = (g.double() * float(np.float32(s))) * lora.double()
+            ref = ref + (g.double() - 1) * base + extra
+            size = size + ((g.double() - 1) * base).abs() + extra.abs()
+        if bias:
+            ref, size = ref + b.double(), size + b.double().abs()
+        bad = (y.double() - ref).abs() > 8 * u * size + U[dt] * ref.abs() + TINY[dt]
+        assert not bool(bad.any()), (T, N, K, dt, int(bad.sum()), bad.nonzero()[:4].tolist())
 
 
 @pytest.mark.parametrize("T,N,K", [(1, 300, 1024), (24, 300, 1024), (24, 301, 1001), (150, 300, 1024), (300, 301, 1001),
