@@ -55,7 +55,7 @@ def _in(t, name: str, device, dtype, shape) -> int:
 def _out(t, name: str, device, dtype, shape, like=None):
     """An output: the caller's, or a new one (like another tensor where there is one of its kind: that is quicker)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device) if like is None else torch.empty_like(like)
+        return torch.empty(*shape, dtype=dtype, device=device) if like is None else torch.empty_like(like)
     _in(t, name, device, dtype, shape)
     return t
 
