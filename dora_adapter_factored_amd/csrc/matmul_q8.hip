@@ -29,6 +29,32 @@ __device__ __forceinline__ i32x4_t load16(const int8_t* p) {
     return v;
 }
 
+// The same by whole dwords, for scattered rows: lanes that each read 16 bytes
+// of another row at odd addresses are split into bytes' worth of requests (4 x
+// 5120 x 27649 took 138 us, 27648 30).  The dwords read are those that hold
+// the 16 bytes, so nothing is touched that shares no aligned dword with them.
+struct Odd16 {
+    i32x4_t lo;
+    int hi, shift;
+};
+
+__device__ __forceinline__ Odd16 load16_dwords(const int8_t* p) {
+    Odd16 v;
+    v.shift = (int)(reinterpret_cast<uintptr_t>(p) & 3);
+    const int* d = reinterpret_cast<const int*>(p - v.shift);
+    __builtin_memcpy(&v.lo, __builtin_assume_aligned(d, 4), 16);
+    v.hi = d[v.shift ? 4 : 3];
+    return v;
+}
+
+__device__ __forceinline__ i32x4_t join(const Odd16& v) {
+    i32x4_t r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        r[i] = (int)__builtin_amdgcn_alignbyte((uint32_t)(i < 3 ? v.lo[i < 3 ? i + 1 : 3] : v.hi), (uint32_t)v.lo[i], (uint32_t)v.shift);
+    return r;
+}
+
 // v without its first n bytes, zeros after them.
 __device__ __forceinline__ i32x4_t drop_bytes(const i32x4_t& v, int n) {
     uint64_t lo = (uint32_t)v[0] | (uint64_t)(uint32_t)v[1] << 32, hi = (uint32_t)v[2] | (uint64_t)(uint32_t)v[3] << 32;
@@ -156,7 +182,7 @@ __global__ __launch_bounds__(kWaves * 64) void q8_one_token(MatmulQ8 a) {
 // would leave most CUs without work (12 x 1024 x 5120: 7.0 us, 64 x 64 tiles
 // in 4 parts 10.4), for rows of fewer than 16 codes, and for up to 16 tokens
 // of codes whose rows are not 4-byte aligned.
-template <typename E>
+template <typename E, bool DWORDS>   // DWORDS: rows are 4-byte aligned
 __global__ __launch_bounds__(kWaves * 64) void q8_direct(MatmulQ8 a) {
     __shared__ int red[kWaves][256];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -173,19 +199,30 @@ __global__ __launch_bounds__(kWaves * 64) void q8_direct(MatmulQ8 a) {
     // U columns at a time, all their loads before the first MFMA
     auto columns = [&](int kb, auto u) __attribute__((always_inline)) {
         constexpr int U = decltype(u)::value;
-        i32x4_t w[U][2], x[U][2];
+        typedef typename std::conditional<DWORDS, i32x4_t, Odd16>::type Codes;
+        Codes w[U][2], x[U][2];
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int k = (kb + i * kWaves) * 128 + kl + j * 16;
-                w[i][j] = load16(wp + k);
-                x[i][j] = load16(xp + k);
+                if constexpr (DWORDS) {
+                    w[i][j] = load16(wp + k);
+                    x[i][j] = load16(xp + k);
+                } else {
+                    w[i][j] = load16_dwords(wp + k);
+                    x[i][j] = load16_dwords(xp + k);
+                }
             }
 #pragma unroll
         for (int i = 0; i < U; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i][j], x[i][j], acc, 0, 0, 0);
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (DWORDS)
+                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i][j], x[i][j], acc, 0, 0, 0);
+                else
+                    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(join(w[i][j]), join(x[i][j]), acc, 0, 0, 0);
+            }
     };
     int kb = wave;
     for (; kb + 3 * kWaves < full; kb += 4 * kWaves) columns(kb, std::integral_constant<int, 4>{});
@@ -760,7 +797,7 @@ hipError_t launch_form(const MatmulQ8& a, int ks, void* workspace, hipStream_t s
 }
 
 template <typename E>
-hipError_t launch_direct(MatmulQ8 a, hipStream_t st) {
+hipError_t launch_direct(MatmulQ8 a, bool dwords, hipStream_t st) {
     const unsigned gx = (unsigned)((a.N + 15) / 16);
     constexpr int64_t kMaxTokens = (int64_t)65535 * 16;   // of one launch: a grid's rows
     const MatmulQ8 all = a;
@@ -770,7 +807,11 @@ hipError_t launch_direct(MatmulQ8 a, hipStream_t st) {
         a.xs = all.xs + t;
         a.lora = all.lora ? static_cast<const E*>(all.lora) + t * all.N : nullptr;
         a.y = static_cast<E*>(all.y) + t * all.N;
-        q8_direct<E><<<dim3(gx, (unsigned)((a.T + 15) / 16)), kWaves * 64, 0, st>>>(a);
+        const dim3 grid(gx, (unsigned)((a.T + 15) / 16));
+        if (dwords)
+            q8_direct<E, true><<<grid, kWaves * 64, 0, st>>>(a);
+        else
+            q8_direct<E, false><<<grid, kWaves * 64, 0, st>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -785,7 +826,7 @@ hipError_t launch_typed(const MatmulQ8& a, void* workspace, hipStream_t st) {
         q8_one_token<E><<<(unsigned)((a.N + kRows - 1) / kRows), kWaves * 64, 0, st>>>(a);
         return hipGetLastError();
     }
-    if (p.form == kDirect) return launch_direct<E>(a, st);
+    if (p.form == kDirect) return launch_direct<E>(a, dma, st);
     switch (p.form) {
         case 0: return launch_form<E, Form0>(a, p.ks, workspace, st);
         case 1: return launch_form<E, Form1>(a, p.ks, workspace, st);
