@@ -440,7 +440,7 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
         return rs;
     };
     const i32x4_t xr = resource(xbase_p, (a.T - t0) * K), wr = resource(wbase_p, (a.N - n0) * K);
-    i32x4_t held[DMA ? 1 : D][DMA ? 1 : LOADS];   // tiles on their way through registers
+    Odd16 held[DMA ? 1 : D][DMA ? 1 : LOADS];   // tiles on their way through registers
     // Each XCD starts its walk over K at its own place, so that rows of one
     // pitch are not all asked for the same columns at once; within an XCD the
     // walks stay together, which its L2 lives on.
@@ -462,7 +462,7 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
             else
                 raw_buffer_load_lds(wr, (lds_void_t*)dst, 16, in ? woff[i < G::XG ? 0 : i - G::XG] : kOutOfRange, k, 0, 0);
         } else {   // past the last tile the first again, which land() turns to zeros: no branch round a load
-            held[slot][i] = load16(row_of(i) + (j < nk ? k : 0) + (i < G::XG ? xchunk : wchunk));
+            held[slot][i] = load16_dwords(row_of(i) + (j < nk ? k : 0) + (i < G::XG ? xchunk : wchunk));
         }
     };
     auto issue = [&](int j, int stage, int slot) __attribute__((always_inline)) {
@@ -476,7 +476,7 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
         if constexpr (!DMA) {
             const int keep = j < nk ? -1 : 0;
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) put(stage, i, held[slot][i] & keep);
+            for (int i = 0; i < LOADS; ++i) put(stage, i, join(held[slot][i]) & keep);
         }
     };
 
@@ -716,8 +716,9 @@ size_t plan_bytes(const Q8Plan& p, int64_t T, int64_t N) {
 
 // The form and number of parts of least cost.  A round of workgroups costs its
 // k-tiles; a launch about 5 us, of which the loads' first latency and the
-// epilogue are most; parts that have to be joined one more launch (3 us) and
-// their bytes written and read again (0.23 us for each MB).  At 333 x 5120 x
+// epilogue are most; parts that have to be joined one more launch (3 us, and
+// for a short call as much again on the host: 4.5) and their bytes written and
+// read again (0.23 us for each MB).  At 333 x 5120 x
 // 27648 this takes 128 x 256 tiles in 4 parts (67 us; without parts 88), at
 // 2048 x 5120 x 5120 192 x 256 tiles (58.5 us; 256 x 256 65.4, 128 x 256
 // 80.9), at 512 x 8192 x 8192 128 x 128 (42.1 us; 128 x 256 54.9, 64 x 128
@@ -731,26 +732,29 @@ int64_t cost_q8(int form, int ks, int64_t T, int64_t N, int64_t K) {
     ns *= nk;
     const int64_t read = N * K / 6300;   // the weight at 6.3 TB/s
     ns = 5000 + (ns > read ? ns : read);
-    if (ks > 1) ns += 3000 + (int64_t)plan_bytes({form, ks}, T, N) / 4400;
+    if (ks > 1) ns += 4500 + (int64_t)plan_bytes({form, ks}, T, N) / 4400;
     return ns;
 }
 
-// 16 channels a workgroup straight from memory, for up to 16 tokens: what a
-// CU's workgroups read at 22.5 GB/s, more with x's rows.
+// 16 channels and tokens a workgroup straight from memory: what a CU's
+// workgroups read at 22.5 GB/s, more with x's rows.
 int64_t cost_direct(int64_t T, int64_t N, int64_t K) {
-    const int64_t rounds = (N + 16 * 256 - 1) / (16 * 256);
-    return 2500 + rounds * 16 * K * (420 + T * T) / 420 * 2 / 45;
+    const int64_t rounds = ((N + 15) / 16 * ((T + 15) / 16) + 255) / 256, t = T < 16 ? T : 16;
+    return 2500 + rounds * 16 * K * (420 + t * t) / 420 * 2 / 45;
 }
 
 Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
     if (T == 1) return {kOneToken, 1};
-    if ((T <= 16 && !dma) || K < 16) return {kDirect, 1};
+    if (K < 16) return {kDirect, 1};
     if (!dma) {
-        // rounds of 256 workgroups: 64 x 64 tiles cost 0.44 us a k-tile, 128 x
-        // 128 about 1.1 (100 x 4099 x 4099: 19.3 us against 35.4; 2000 x 4099
-        // x 4099: 150 against 121)
+        // by rounds of 256 workgroups: 64 x 64 tiles cost 0.43 us a k-tile,
+        // 128 x 128 1.22 (1000 x 4099 x 4099: 70 us against 82; 1500 x 12001 x
+        // 4097: 270 against 217), and straight from memory 24 x 1025 x 5121
+        // takes 10 us, tiles 20
         auto rounds = [&](int64_t b) { return (((T + b - 1) / b) * ((N + b - 1) / b) + 255) / 256; };
-        return {rounds(64) * 2 <= rounds(128) * 5 ? kRegsSmall : kRegsBig, 1};
+        const int64_t nk = (K + 127) / 128, small = 5000 + rounds(64) * 430 * nk, big = 5000 + rounds(128) * 1220 * nk;
+        const int64_t direct = T <= 48 ? cost_direct(T, N, K) : INT64_MAX;
+        return {direct < small && direct < big ? kDirect : small <= big ? kRegsSmall : kRegsBig, 1};
     }
     Q8Plan best{kDirect, 1};
     int64_t least = T <= 16 ? cost_direct(T, N, K) : INT64_MAX;
