@@ -359,6 +359,7 @@ int check_workspace(const void* workspace, size_t have, size_t need) {
 
 // int32 holds any sum of this many products of two bytes: 131071 * 2^14 < 2^31
 constexpr int64_t kMaxQ8Depth = 131071;
+constexpr int64_t kMaxQ8Channels = (int64_t)1 << 24;   // a grid's threads are counted in 32 bits
 
 int check_q8_sizes(int64_t T, int64_t d_out, int64_t d_in) {
     if (!dim_ok(T, 0) || !dim_ok(d_out, 1) || !dim_ok(d_in, 1))
@@ -367,6 +368,9 @@ int check_q8_sizes(int64_t T, int64_t d_out, int64_t d_in) {
     if (d_in > kMaxQ8Depth)
         return fail(DORA_ERR_UNSUPPORTED, "d_in is %lld; an int32 sum holds at most %lld products", (long long)d_in,
                     (long long)kMaxQ8Depth);
+    if (d_out > kMaxQ8Channels)
+        return fail(DORA_ERR_UNSUPPORTED, "d_out is %lld; at most %lld channels are supported", (long long)d_out,
+                    (long long)kMaxQ8Channels);
     return DORA_OK;
 }
 

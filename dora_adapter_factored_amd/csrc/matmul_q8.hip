@@ -552,7 +552,7 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
 #pragma unroll
             for (int s = 0; s < S; ++s) issue(s, s * G::STAGE, 0);
             wait_vmcnt<(S - 1) * LOADS>();
-            __builtin_amdgcn_s_barrier();
+            lds_barrier();
         } else {
 #pragma unroll
             for (int s = 0; s < D; ++s) issue(s, 0, s);
@@ -582,8 +582,7 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
                 }
                 if constexpr (DMA) {
                     wait_vmcnt<(S - 2) * LOADS>();
-                    wait_lgkmcnt0();
-                    __builtin_amdgcn_s_barrier();
+                    lds_barrier();
                 } else {
                     land(j + 1, next, slot);   // the readers of that stage's last tile passed the last barrier
                     __syncthreads();
@@ -800,37 +799,14 @@ hipError_t launch_form(const MatmulQ8& a, int ks, void* workspace, hipStream_t s
     return hipGetLastError();
 }
 
-template <typename E>
-hipError_t launch_direct(MatmulQ8 a, bool dwords, hipStream_t st) {
-    const unsigned gx = (unsigned)((a.N + 15) / 16);
-    constexpr int64_t kMaxTokens = (int64_t)65535 * 16;   // of one launch: a grid's rows
-    const MatmulQ8 all = a;
-    for (int64_t t = 0; t < all.T; t += kMaxTokens) {
-        a.T = all.T - t < kMaxTokens ? all.T - t : kMaxTokens;
-        a.xq = all.xq + t * all.K;
-        a.xs = all.xs + t;
-        a.lora = all.lora ? static_cast<const E*>(all.lora) + t * all.N : nullptr;
-        a.y = static_cast<E*>(all.y) + t * all.N;
-        const dim3 grid(gx, (unsigned)((a.T + 15) / 16));
-        if (dwords)
-            q8_direct<E, true><<<grid, kWaves * 64, 0, st>>>(a);
-        else
-            q8_direct<E, false><<<grid, kWaves * 64, 0, st>>>(a);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
-}
+// Tokens of one launch: a grid has at most 65535 rows (16 tokens each straight
+// from memory), and with at most 2^24 channels its threads stay below 2^32.
+constexpr int64_t kPieceTokens = (int64_t)1 << 19;
 
 template <typename E>
-hipError_t launch_typed(const MatmulQ8& a, void* workspace, hipStream_t st) {
+hipError_t launch_piece(const MatmulQ8& a, void* workspace, hipStream_t st) {
     const bool dma = a.K % 4 == 0 && aligned_to(a.xq, 4) && aligned_to(a.wq, 4);
     const Q8Plan p = plan_q8(a.T, a.N, a.K, dma);
-    if (p.form == kOneToken) {
-        q8_one_token<E><<<(unsigned)((a.N + kRows - 1) / kRows), kWaves * 64, 0, st>>>(a);
-        return hipGetLastError();
-    }
-    if (p.form == kDirect) return launch_direct<E>(a, dma, st);
     switch (p.form) {
         case 0: return launch_form<E, Form0>(a, p.ks, workspace, st);
         case 1: return launch_form<E, Form1>(a, p.ks, workspace, st);
@@ -839,18 +815,46 @@ hipError_t launch_typed(const MatmulQ8& a, void* workspace, hipStream_t st) {
         case 4: return launch_form<E, Form4>(a, p.ks, workspace, st);
         case 5: return launch_form<E, Form5>(a, p.ks, workspace, st);
         case kRegsBig: return launch_form<E, FormR0>(a, 1, workspace, st);
-        default: return launch_form<E, FormR1>(a, 1, workspace, st);
+        case kRegsSmall: return launch_form<E, FormR1>(a, 1, workspace, st);
+        default: break;
     }
+    if (p.form == kOneToken) {
+        q8_one_token<E><<<(unsigned)((a.N + kRows - 1) / kRows), kWaves * 64, 0, st>>>(a);
+        return hipGetLastError();
+    }
+    const dim3 grid((unsigned)((a.N + 15) / 16), (unsigned)((a.T + 15) / 16));
+    if (dma)
+        q8_direct<E, true><<<grid, kWaves * 64, 0, st>>>(a);
+    else
+        q8_direct<E, false><<<grid, kWaves * 64, 0, st>>>(a);
+    return hipGetLastError();
+}
+
+template <typename E>
+hipError_t launch_typed(const MatmulQ8& a, void* workspace, hipStream_t st) {
+    MatmulQ8 b = a;
+    for (int64_t t = 0; t < a.T; t += kPieceTokens) {
+        b.T = a.T - t < kPieceTokens ? a.T - t : kPieceTokens;
+        b.xq = a.xq + t * a.K;
+        b.xs = a.xs + t;
+        b.lora = a.lora ? static_cast<const E*>(a.lora) + t * a.N : nullptr;
+        b.y = static_cast<E*>(a.y) + t * a.N;
+        const hipError_t e = launch_piece<E>(b, workspace, st);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace
 
 size_t matmul_q8_workspace_bytes(int64_t T, int64_t N, int64_t K) {
-    // the codes' alignment is known only at the call
+    // the largest of the pieces'; only the forms of 4-byte aligned rows have
+    // parts, and whether codes are is known at the call
     size_t most = 0;
-    for (int dma = 0; dma < 2; ++dma) {
-        if (dma && K % 4 != 0) continue;
-        const size_t b = plan_bytes(plan_q8(T, N, K, dma), T, N);
+    const int64_t pieces[2] = {T < kPieceTokens ? T : kPieceTokens, T % kPieceTokens};
+    for (int64_t t : pieces) {
+        if (t == 0 || K % 4 != 0) continue;
+        const size_t b = plan_bytes(plan_q8(t, N, K, true), t, N);
         most = b > most ? b : most;
     }
     return align_up(most, 256);

@@ -76,7 +76,7 @@ MM = dict(xq=FAKE, xs=FAKE, wq=OTHER, ws=FAKE, bias=None, g=None, lora=None, s=1
 @pytest.mark.parametrize("kw,status", [
     (dict(xq=None), INV), (dict(xs=None), INV), (dict(wq=None), INV), (dict(y=None), INV), (dict(g=FAKE), INV),
     (dict(lora=FAKE), INV), (dict(s=float("nan")), INV), (dict(T=-1), INV), (dict(T=BIG), INV), (dict(N=0), INV),
-    (dict(N=BIG), INV), (dict(K=0), INV), (dict(K=131072), UNS), (dict(dtype=4), INV), (dict(y=FAKE), INV),
+    (dict(N=BIG), INV), (dict(N=(1 << 24) + 1), UNS), (dict(K=0), INV), (dict(K=131072), UNS), (dict(dtype=4), INV), (dict(y=FAKE), INV),
     (dict(y=OTHER), INV),
 ])
 def test_matmul_q8_refuses(lib, kw, status):

@@ -454,6 +454,22 @@ def test_matmul_q8_offsets_past_32_bits():
     assert y.numel() > 2 ** 31 and torch.equal(y[-70:], tail)
 
 
+@pytest.mark.parametrize("N,K", [(40, 64), (17, 9)])
+def test_matmul_q8_more_tokens_than_one_launch_takes(N, K):
+    say(f"[matmul_q8] many tokens, {N}x{K}")
+    T = (1 << 19) + 70
+    g = rng(N)
+    xq = torch.randint(-127, 128, (T, K), generator=g, device=DEV, dtype=torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    xs, ws = torch.rand(T, generator=g, device=DEV), torch.rand(N, generator=g, device=DEV)
+    gg, lora = torch.rand(N, generator=g, device=DEV), randn(g, T, N)
+    y = D.matmul_q8(xq, xs, wq, ws, torch.float32, g=gg, lora_out=lora, s=0.5)
+    base = (xq.double() @ wq.double().t()) * xs.double()[:, None] * ws.double()
+    extra = (gg.double() * 0.5) * lora.double()
+    bad = (y.double() - (gg.double() * base + extra)).abs() > 9 * u * (3 * base.abs() + extra.abs()) + TINY["f32"]
+    assert not bool(bad.any())
+
+
 # ------------------------------------------------------------------ a training step's frozen weight
 @pytest.mark.parametrize("T,N,K", [(1, 64, 96), (70, 130, 200), (300, 512, 384)])
 def test_linear_q8_and_its_gradient(T, N, K):
