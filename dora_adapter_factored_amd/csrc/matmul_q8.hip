@@ -318,8 +318,10 @@ __device__ __forceinline__ i32x4_t* part_at(const TileGrid& g, int part, int tm,
 // Workgroup id -> part of K and tile.  Ids go round the XCDs, so XCD x takes
 // the x-th contiguous part of the order, in which kGroupM token tiles share a
 // channel tile before the next one: the tiles an XCD works on at one time are
-// a block, whose operands' rows meet in its L2.
-constexpr int kGroupM = 8;
+// a block, whose operands' rows meet in its L2.  4 x 8 tiles of 256 x 256: 737
+// us at 4096 x 28672 x 8192, 8 x 4 744, 2 x 16 and 3 x 11 about 760 to 775, 16
+// x 2 772.
+constexpr int kGroupM = 4;
 
 __device__ __forceinline__ void tile_of(int id, const TileGrid& g, int& part, int& m, int& n) {
     const int tiles = g.tm * g.tn, total = tiles * g.ks, q = total / kNumXCD, r = total % kNumXCD;
@@ -332,6 +334,15 @@ __device__ __forceinline__ void tile_of(int id, const TileGrid& g, int& part, in
     m = grp * kGroupM + rest % h;
     n = rest / h;
 }
+
+// What bounds the tile forms, on MI355X.  256 x 256 over the whole chip: power
+// and the operands' way to the CU.  Of the cycles at 4096 x 28672 x 8192 the
+// matrix units are busy in 66% (SQ_VALU_MFMA_BUSY_CYCLES), at 1.85 GHz of
+// 2.4; with every load a hit in L2 the product is 6 to 9% faster, LDS has no
+// bank conflicts (with them: 1% slower), and 4 waves of 128 x 128 with a third
+// fewer LDS reads are no faster.  The small forms: the latency of a k-tile's
+// barrier, fragment reads and loads in one workgroup (290 ns for 64 x 64),
+// which a second workgroup on the CU hides.
 
 // Results of wave (wt, wc) of the tile at (t0, n0), token blocks m_begin ..
 // m_end - 1: lane l has token l % 16 of a block and the 16 channels from 16 (l
@@ -509,11 +520,18 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
             }
         }
     };
+    // back and forth, so that each MFMA has an operand of the one before it: the
+    // full chip runs against its power limit (1.85 GHz at 4096 x 28672 x 8192,
+    // 4.0 POP/s with operands in registers and nothing else, 4.9 with zeros in
+    // them), and fewer toggled inputs are 1 to 1.7% of the time there
     auto mma = [&](const i32x4_t (&x)[G::MT], const i32x4_t (&w)[G::NC]) __attribute__((always_inline)) {
 #pragma unroll
         for (int m = 0; m < G::MT; ++m)
 #pragma unroll
-            for (int c = 0; c < G::NC; ++c) acc[m][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[c], x[m], acc[m][c], 0, 0, 0);
+            for (int i = 0; i < G::NC; ++i) {
+                const int c = m % 2 ? G::NC - 1 - i : i;
+                acc[m][c] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[c], x[m], acc[m][c], 0, 0, 0);
+            }
     };
     // Reads, and the second step's loads, are spread over the MFMAs: the reads
     // run under the matrix pipe, and a wave's loads wait their turn at the
