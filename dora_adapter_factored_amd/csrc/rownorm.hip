@@ -5,10 +5,11 @@
 // Forward, row t of [T, d], all in fp32, each output rounded once:
 //   h = x + residual,  rstd = 1 / sqrt(mean_j h_j^2 + eps),  y = h rstd w
 //   scale = max_j |y_j| / 127,  q_j = rint(y_j / scale)
-// rstd cancels in q: with p = h w and a = max_j |p_j|, q_j = rint(p_j 127 / a)
-// and scale = a rstd / 127, so the codes need one maximum over products that
-// are at hand in the same pass as the sum of squares, and the row is read
-// once.  Rows to 8 bits are the same with rstd = 1 and w the column scale.
+// The codes are those of the fp32 y, with the division rounded as IEEE has it:
+// an outlier channel makes a code's step a large part of a row's rms, and a
+// code that falls the other way at a tie is seen.  (One reduction would do, as
+// rstd cancels in y / scale; it saved nothing, the row's bytes being what
+// counts.)  Rows to 8 bits are the same with rstd = 1 and w the column scale.
 //
 // Backward, from dy into y and dh into h (rstd kept by the forward pass):
 //   u = w dy,  dx = rstd (u - h rstd^2 mean_j(u_j h_j)) + dh,  dw_j = sum_t dy h rstd
@@ -28,8 +29,8 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 constexpr uint32_t kInfBits = 0x7f800000u;
-// Rows whose largest value is below 2^-119 quantise to zeros with scale 0:
-// 127 / a would leave the fp32 range there.  The error is below 2^-119.
+// Rows whose largest value is below 2^-119 quantise to zeros with scale 0: the
+// scale would be subnormal there.  The error is below 2^-119.
 constexpr uint32_t kTinyBits = (uint32_t)(127 - 119) << 23;
 
 // Rows go in packs of 16 bytes.  Aligned rows (AL: pointers and row pitch
@@ -86,13 +87,30 @@ __device__ __forceinline__ void load_w(const W* w, int64_t left, float (&v)[N]) 
     }
 }
 
-// N codes: rint(p inv) packed into bytes.  |p inv| <= 127 up to one rounding,
-// which rint takes back to 127.
+// What the codes of a row divide by: scale and its reciprocal, both 0 where
+// the codes are 0 (scale 0 or NaN).
+struct Divisor {
+    float scale, recip;
+};
+
+__device__ __forceinline__ Divisor divisor(float scale) {
+    return scale > 0.0f ? Divisor{scale, 1.0f / scale} : Divisor{0.0f, 0.0f};
+}
+
+// N codes: rint(p / scale) packed into bytes.  |p / scale| <= 127 up to a
+// rounding or two, which rint takes back to 127.  The quotient is Markstein's:
+// p times the reciprocal, corrected by its remainder, which is p / scale
+// correctly rounded (a division for each element took 22.6 us at 4096 x 8192
+// where this takes 18).
 template <bool AL, int N>
-__device__ __forceinline__ void store_codes(int8_t* q, const float (&p)[N], float inv, int64_t left) {
+__device__ __forceinline__ void store_codes(int8_t* q, const float (&p)[N], const Divisor& by, int64_t left) {
     int c[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) c[e] = (int)rintf(p[e] * inv);
+    for (int e = 0; e < N; ++e) {
+        const float v = by.recip == 0.0f ? 0.0f : p[e];   // not a NaN's or an infinity's product with 0
+        const float quot = v * by.recip;
+        c[e] = (int)rintf(fmaf(fmaf(-quot, by.scale, v), by.recip, quot));
+    }
     uint32_t u[N / 4];
 #pragma unroll
     for (int i = 0; i < N / 4; ++i)
@@ -108,41 +126,40 @@ __device__ __forceinline__ void store_codes(int8_t* q, const float (&p)[N], floa
     }
 }
 
-// (sum, maximum) over the workgroup, returned to every thread.  Sums are
-// added in a fixed order.  red holds kMaxWaves entries of each and is free to
-// be written again after the next barrier.
-__device__ __forceinline__ void block_reduce(float& sum, uint32_t& top, float* rs, uint32_t* rt) {
+// The sum or the maximum over the workgroup, returned to every thread.  Sums
+// are added in a fixed order.  red holds kMaxWaves entries and is free to be
+// written again after the next barrier.
+template <typename V, typename Op>
+__device__ __forceinline__ V block_reduce(V v, V* red, Op op) {
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-        sum += __shfl_xor(sum, o);
-        const uint32_t t = __shfl_xor(top, o);
-        top = t > top ? t : top;
-    }
+    for (int o = 32; o > 0; o >>= 1) v = op(v, __shfl_xor(v, o));
     const int nw = blockDim.x >> 6;
-    if (nw == 1) return;
-    const int w = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
-        rs[w] = sum;
-        rt[w] = top;
-    }
+    if (nw == 1) return v;
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
     __syncthreads();
-    sum = rs[0];
-    top = rt[0];
-    for (int i = 1; i < nw; ++i) {
-        sum += rs[i];
-        top = rt[i] > top ? rt[i] : top;
-    }
+    v = red[0];
+    for (int i = 1; i < nw; ++i) v = op(v, red[i]);
+    return v;
 }
 
-// What a row's codes need: the factor of p, and the row's scale.  A row that
-// holds a NaN or an infinity has scale NaN and codes 0, so all that comes of
-// it is NaN.
-__device__ __forceinline__ void code_scale(uint32_t top, float rstd, float& inv, float& scale) {
-    const float a = __uint_as_float(top);
-    const bool tiny = top < kTinyBits, bad = top >= kInfBits;
-    inv = tiny || bad ? 0.0f : 127.0f / a;
-    scale = bad ? __uint_as_float(0x7fc00000u) : tiny ? 0.0f : a * rstd / 127.0f;
+__device__ __forceinline__ float block_sum(float v, float* red) {
+    return block_reduce(v, red, [](float a, float b) { return a + b; });
 }
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+    return block_reduce(v, red, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+
+// |v|'s bits, whose order as integers is the values', NaN above infinity.
+__device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// A row's scale from the bits of its largest |value|.  A row that holds a NaN
+// or an infinity has scale NaN (and codes 0), so all that comes of it is NaN.
+__device__ __forceinline__ float code_scale(uint32_t top) {
+    return top >= kInfBits ? __uint_as_float(0x7fc00000u) : top < kTinyBits ? 0.0f : __uint_as_float(top) * (1.0f / 127.0f);
+}
+
+__device__ __forceinline__ float row_rstd(float sum, int64_t d, float eps) { return rsqrtf(sum * (1.0f / (float)d) + eps); }
 
 struct RowArgs {
     const void* x;
@@ -157,15 +174,6 @@ struct RowArgs {
     float* rstd;
 };
 
-// Codes of a row with a NaN or infinity: 0 whatever p is (NaN * 0 is NaN, and
-// a NaN's conversion to an integer is not to be relied on).
-template <int N>
-__device__ __forceinline__ void zero_unless(bool keep, float (&p)[N]) {
-    if (keep) return;
-#pragma unroll
-    for (int e = 0; e < N; ++e) p[e] = 0.0f;
-}
-
 // One row per workgroup, the row in registers.  NORM: the norm (w of type E,
 // outputs h, y, q, rstd as asked); otherwise rows to 8 bits (w an optional
 // fp32 column scale).
@@ -178,7 +186,7 @@ __global__ __launch_bounds__(P > 4 ? 512 : 1024) void row_regs(RowArgs a) {
     const E* x = static_cast<const E*>(a.x) + off;
     const W* w = static_cast<const W*>(a.w);
     const int d = (int)a.d, n = (d + N - 1) / N, nt = blockDim.x;
-    float v[P][N], p[P][N];
+    float v[P][N];
     {
         Pack<E> xv[P], rv[P];
 #pragma unroll
@@ -199,50 +207,48 @@ __global__ __launch_bounds__(P > 4 ? 512 : 1024) void row_regs(RowArgs a) {
             }
         }
     }
-    float sum = 0.0f;
+    float rstd = 1.0f;
+    if (NORM) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int k = threadIdx.x + i * nt;
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum = fmaf(v[i][e], v[i][e], sum);
+            if (a.h && k < n) store_row<E, AL>(static_cast<E*>(a.h) + off + k * N, v[i], d - k * N);
+        }
+        rstd = row_rstd(block_sum(sum, rs), a.d, a.eps);
+        if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
+    }
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
+    for (int i = 0; i < P; ++i) {   // v becomes y
         const int k = threadIdx.x + i * nt;
+        if (k >= n) continue;
         float wv[N];
 #pragma unroll
         for (int e = 0; e < N; ++e) wv[e] = 1.0f;
-        if (k < n && w) load_w<W, AL>(w + k * N, d - k * N, wv);
+        if (w) load_w<W, AL>(w + k * N, d - k * N, wv);
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-            if (NORM) sum = fmaf(v[i][e], v[i][e], sum);
-            p[i][e] = k < n ? v[i][e] * wv[e] : 0.0f;
-            const uint32_t m = __float_as_uint(p[i][e]) & 0x7fffffffu;
+            v[i][e] = (v[i][e] * rstd) * wv[e];
+            const uint32_t m = magnitude(v[i][e]);
             top = m > top ? m : top;
         }
-        if (NORM && a.h && k < n) store_row<E, AL>(static_cast<E*>(a.h) + off + k * N, v[i], d - k * N);
+        if (NORM && a.y) store_row<E, AL>(static_cast<E*>(a.y) + off + k * N, v[i], d - k * N);
     }
-    block_reduce(sum, top, rs, rt);
-    const float rstd = NORM ? 1.0f / sqrtf(sum / (float)a.d + a.eps) : 1.0f;
-    float inv, scale;
-    code_scale(top, rstd, inv, scale);
-    if (threadIdx.x == 0) {
-        if (NORM && a.rstd) a.rstd[row] = rstd;
-        if (a.q) a.scale[row] = scale;
-    }
+    if (!a.q) return;
+    const float scale = code_scale(block_max(top, rt));
+    if (threadIdx.x == 0) a.scale[row] = scale;
+    const Divisor by = divisor(scale);
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int k = threadIdx.x + i * nt;
-        if (k >= n) continue;
-        if (NORM && a.y) {
-            float yv[N];
-#pragma unroll
-            for (int e = 0; e < N; ++e) yv[e] = p[i][e] * rstd;
-            store_row<E, AL>(static_cast<E*>(a.y) + off + k * N, yv, d - k * N);
-        }
-        if (a.q) {
-            zero_unless<N>(inv != 0.0f, p[i]);
-            store_codes<AL>(a.q + off + k * N, p[i], inv, d - k * N);
-        }
+        if (k < n) store_codes<AL>(a.q + off + k * N, v[i], by, d - k * N);
     }
 }
 
-// The same for rows of any length, read twice.
+// The same for rows of any length, read once for each of their passes.
 template <typename E, typename W, bool AL, bool NORM>
 __global__ __launch_bounds__(1024) void row_long(RowArgs a) {
     constexpr int N = Pack<E>::N;
@@ -252,7 +258,7 @@ __global__ __launch_bounds__(1024) void row_long(RowArgs a) {
     const E* x = static_cast<const E*>(a.x) + off;
     const E* r = NORM && a.res ? static_cast<const E*>(a.res) + off : nullptr;
     const W* w = static_cast<const W*>(a.w);
-    auto pack = [&](int64_t k, float (&v)[N], float (&p)[N]) __attribute__((always_inline)) {
+    auto sum_at = [&](int64_t k, float (&v)[N]) __attribute__((always_inline)) {
         Pack<E> t = load_row<E, AL>(x + k * N, a.d - k * N);
 #pragma unroll
         for (int e = 0; e < N; ++e) v[e] = at(t, e);
@@ -261,49 +267,54 @@ __global__ __launch_bounds__(1024) void row_long(RowArgs a) {
 #pragma unroll
             for (int e = 0; e < N; ++e) v[e] += at(t, e);
         }
-#pragma unroll
-        for (int e = 0; e < N; ++e) p[e] = 1.0f;
-        if (w) load_w<W, AL>(w + k * N, a.d - k * N, p);
-#pragma unroll
-        for (int e = 0; e < N; ++e) p[e] *= v[e];
     };
-    float sum = 0.0f;
-    uint32_t top = 0;
-    for (int64_t k = threadIdx.x; k < n; k += blockDim.x) {
-        float v[N], p[N];
-        pack(k, v, p);
+    auto scaled = [&](int64_t k, float (&v)[N], float rstd) __attribute__((always_inline)) {
+        float wv[N];
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-            if (NORM) sum = fmaf(v[e], v[e], sum);
-            const uint32_t m = __float_as_uint(p[e]) & 0x7fffffffu;
-            top = m > top ? m : top;
+        for (int e = 0; e < N; ++e) wv[e] = 1.0f;
+        if (w) load_w<W, AL>(w + k * N, a.d - k * N, wv);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = (v[e] * rstd) * wv[e];
+    };
+    float rstd = 1.0f;
+    if (NORM) {
+        float sum = 0.0f;
+        for (int64_t k = threadIdx.x; k < n; k += blockDim.x) {
+            float v[N];
+            sum_at(k, v);
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum = fmaf(v[e], v[e], sum);
         }
+        rstd = row_rstd(block_sum(sum, rs), a.d, a.eps);
+        if (threadIdx.x == 0 && a.rstd) a.rstd[row] = rstd;
     }
-    block_reduce(sum, top, rs, rt);
-    const float rstd = NORM ? 1.0f / sqrtf(sum / (float)a.d + a.eps) : 1.0f;
-    float inv, scale;
-    code_scale(top, rstd, inv, scale);
-    if (threadIdx.x == 0) {
-        if (NORM && a.rstd) a.rstd[row] = rstd;
-        if (a.q) a.scale[row] = scale;
+    float scale = 0.0f;
+    if (a.q) {
+        uint32_t top = 0;
+        for (int64_t k = threadIdx.x; k < n; k += blockDim.x) {
+            float v[N];
+            sum_at(k, v);
+            scaled(k, v, rstd);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const uint32_t m = magnitude(v[e]);
+                top = m > top ? m : top;
+            }
+        }
+        scale = code_scale(block_max(top, rt));
+        if (threadIdx.x == 0) a.scale[row] = scale;
     }
+    const Divisor by = divisor(scale);
     // each element is read by the thread that writes it, so h may be x or the
     // residual itself
     for (int64_t k = threadIdx.x; k < n; k += blockDim.x) {
-        float v[N], p[N];
-        pack(k, v, p);
+        float v[N];
+        sum_at(k, v);
         const int64_t left = a.d - k * N;
         if (NORM && a.h) store_row<E, AL>(static_cast<E*>(a.h) + off + k * N, v, left);
-        if (NORM && a.y) {
-            float yv[N];
-#pragma unroll
-            for (int e = 0; e < N; ++e) yv[e] = p[e] * rstd;
-            store_row<E, AL>(static_cast<E*>(a.y) + off + k * N, yv, left);
-        }
-        if (a.q) {
-            zero_unless<N>(inv != 0.0f, p);
-            store_codes<AL>(a.q + off + k * N, p, inv, left);
-        }
+        scaled(k, v, rstd);
+        if (NORM && a.y) store_row<E, AL>(static_cast<E*>(a.y) + off + k * N, v, left);
+        if (a.q) store_codes<AL>(a.q + off + k * N, v, by, left);
     }
 }
 
@@ -330,7 +341,6 @@ __global__ __launch_bounds__(P < 4 ? 1024 : P == 4 ? 512 : 640) void rms_bwd_reg
     constexpr int N = Pack<E>::N;
     constexpr bool WIDE = P > 4;
     __shared__ float rs[2][kMaxWaves];
-    __shared__ uint32_t rt[2][kMaxWaves];
     const int d = (int)a.d, n = (d + N - 1) / N, nt = blockDim.x;
     const E* w = static_cast<const E*>(a.w);
     Pack<E> wv[WIDE ? 1 : P];
@@ -358,7 +368,6 @@ __global__ __launch_bounds__(P < 4 ? 1024 : P == 4 ? 512 : 640) void rms_bwd_reg
         }
         const float r = a.rstd[row];
         float c = 0.0f;
-        uint32_t none = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             const int k = threadIdx.x + i * nt;
@@ -371,8 +380,7 @@ __global__ __launch_bounds__(P < 4 ? 1024 : P == 4 ? 512 : 640) void rms_bwd_reg
                 dw[i][e] = fmaf(dv, hh * r, dw[i][e]);
             }
         }
-        block_reduce(c, none, rs[par], rt[par]);
-        const float f = c / (float)a.d * r * r;
+        const float f = block_sum(c, rs[par]) / (float)a.d * r * r;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
             // the row is kept as it was loaded: without this the compiler
@@ -411,7 +419,6 @@ __global__ __launch_bounds__(P < 4 ? 1024 : P == 4 ? 512 : 640) void rms_bwd_reg
 template <typename E>
 __global__ __launch_bounds__(1024) void rms_bwd_long(BwdArgs a) {
     __shared__ float rs[kMaxWaves];
-    __shared__ uint32_t rt[kMaxWaves];
     const int64_t row = a.row0 + blockIdx.x, off = row * a.d;
     const E* dy = static_cast<const E*>(a.dy) + off;
     const E* h = static_cast<const E*>(a.h) + off;
@@ -419,11 +426,9 @@ __global__ __launch_bounds__(1024) void rms_bwd_long(BwdArgs a) {
     const E* w = static_cast<const E*>(a.w);
     const float r = a.rstd[row];
     float c = 0.0f;
-    uint32_t none = 0;
     for (int64_t k = threadIdx.x; k < a.d; k += blockDim.x)
         c = fmaf(Cvt<E>::to_f(dy[k]) * Cvt<E>::to_f(w[k]), Cvt<E>::to_f(h[k]), c);
-    block_reduce(c, none, rs, rt);
-    const float f = c / (float)a.d * r * r;
+    const float f = block_sum(c, rs) / (float)a.d * r * r;
     for (int64_t k = threadIdx.x; k < a.d; k += blockDim.x) {
         const float u = Cvt<E>::to_f(dy[k]) * Cvt<E>::to_f(w[k]);
         const float o = r * (u - Cvt<E>::to_f(h[k]) * f) + (dh ? Cvt<E>::to_f(dh[k]) : 0.0f);
