@@ -332,12 +332,12 @@ struct BwdArgs {
 };
 
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ... of one workgroup, each in
-// registers between its reduction and its store.  Six accesses a thread, for
-// the longest rows, leave no registers for w and dh: they are loaded where
-// they are used (registers that spill cost more: 60 us instead of 18 at 2048
+// registers between its reduction and its store.  Six accesses a thread (eight
+// of fp32), for the longest rows, leave no registers for w and dh: they are
+// loaded where they are used (registers that spill cost more: 60 us instead of 18 at 2048
 // x 5120 when 4 accesses were held to 128).
 template <typename E, bool AL, int P>
-__global__ __launch_bounds__(P < 4 ? 1024 : P == 4 ? 512 : 640) void rms_bwd_regs(BwdArgs a) {
+__global__ __launch_bounds__(P == 4 ? 512 : P == 6 ? 640 : 1024) void rms_bwd_regs(BwdArgs a) {
     constexpr int N = Pack<E>::N;
     constexpr bool WIDE = P > 4;
     __shared__ float rs[2][kMaxWaves];
@@ -605,13 +605,14 @@ int bwd_parts(int64_t rows) {
 template <typename E, bool AL>
 bool launch_bwd_regs(const BwdArgs& a, int parts, hipStream_t st) {
     const int64_t n = (a.d + Pack<E>::N - 1) / Pack<E>::N;
-    const RowShape s = n <= 4 * 512 ? row_shape(n, a.rows, 4) : RowShape{6, (int)(((n + 5) / 6 + 63) / 64 * 64)};
-    if (n > 6 * 640) return false;
+    constexpr int LONG = sizeof(E) == 4 ? 8 : 6;   // accesses a thread of the longest rows
+    if (n > LONG * (LONG == 8 ? 1024 : 640)) return false;
+    const RowShape s = n <= 4 * 512 ? row_shape(n, a.rows, 4) : RowShape{LONG, (int)(((n + LONG - 1) / LONG + 63) / 64 * 64)};
     switch (s.p) {
         case 1: rms_bwd_regs<E, AL, 1><<<parts, s.nt, 0, st>>>(a); break;
         case 2: rms_bwd_regs<E, AL, 2><<<parts, s.nt, 0, st>>>(a); break;
         case 4: rms_bwd_regs<E, AL, 4><<<parts, s.nt, 0, st>>>(a); break;
-        default: rms_bwd_regs<E, AL, 6><<<parts, s.nt, 0, st>>>(a); break;
+        default: rms_bwd_regs<E, AL, LONG><<<parts, s.nt, 0, st>>>(a); break;
     }
     return true;
 }
