@@ -180,8 +180,9 @@ __global__ __launch_bounds__(kWaves * 64) void q8_one_token(MatmulQ8 a) {
 // K in turn straight from memory into the MFMA operands; the waves' sums are
 // added through LDS.  For few tokens and channels, where tiles through LDS
 // would leave most CUs without work (12 x 1024 x 5120: 7.0 us, 64 x 64 tiles
-// in 4 parts 10.4), for rows of fewer than 16 codes, and for up to 16 tokens
-// of codes whose rows are not 4-byte aligned.
+// in 4 parts 10.4), for rows of fewer than 16 codes, and for few tokens of
+// codes whose rows are not 4-byte aligned.  8 x 8192 x 8192: 16.5 us, 4.1 TB/s;
+// 64-byte requests hold a CU to 22.5 GB/s.
 template <typename E, bool DWORDS>   // DWORDS: rows are 4-byte aligned
 __global__ __launch_bounds__(kWaves * 64) void q8_direct(MatmulQ8 a) {
     __shared__ int red[kWaves][256];
@@ -464,7 +465,7 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
     };
     // load i of the walk's tile j; past the last one: nothing that anyone reads
     auto issue_one = [&](int j, int stage, int slot, int i) __attribute__((always_inline)) {
-        const int k = tile_at(j) * 128;
+        const int k = j < nk ? tile_at(j) * 128 : 0;   // a buffer's scalar offset stays inside it
         if constexpr (DMA) {
             const bool in = j < nk && k + (i < G::XG ? xchunk : wchunk) < K;
             char* dst = smem + stage + wave * 1024 + i * G::NW * 1024;   // the channels' rows follow the tokens'
@@ -473,7 +474,7 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
             else
                 raw_buffer_load_lds(wr, (lds_void_t*)dst, 16, in ? woff[i < G::XG ? 0 : i - G::XG] : kOutOfRange, k, 0, 0);
         } else {   // past the last tile the first again, which land() turns to zeros: no branch round a load
-            held[slot][i] = load16_dwords(row_of(i) + (j < nk ? k : 0) + (i < G::XG ? xchunk : wchunk));
+            held[slot][i] = load16_dwords(row_of(i) + k + (i < G::XG ? xchunk : wchunk));
         }
     };
     auto issue = [&](int j, int stage, int slot) __attribute__((always_inline)) {
@@ -668,7 +669,9 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
 }
 
 // The parts of K joined, and the epilogue: a wave for each token block of a
-// tile's wave.  Integer sums: any order is exact.
+// tile's wave.  Integer sums: any order is exact.  Bound by the parts' bytes
+// (134 MB of 2048 x 8192 x 8192 in two parts: 35 us more than one part's
+// epilogue; in row order, 16 bytes of 64 rows at a time, it took 150).
 template <typename E, typename G, bool VEC>
 __global__ __launch_bounds__(256) void q8_join(MatmulQ8 a, TileGrid grid) {
     const int lane = threadIdx.x & 63;
