@@ -695,6 +695,20 @@ __global__ __launch_bounds__(256) void q8_join(MatmulQ8 a, TileGrid grid) {
         store_results<E, G, VEC, false>(a, t0, n0, wave / G::WC, wave % G::WC, m, m + 1, [&](int, int cg, int b) { return sum[cg * 4 + b]; });
 }
 
+// Rows of K codes to rows of Kp, a multiple of 16, zeros after the codes: x's T
+// rows, then w's N.
+__global__ __launch_bounds__(256) void q8_pad(MatmulQ8 a, int Kp, int8_t* __restrict__ xp, int8_t* __restrict__ wp) {
+    const int K = (int)a.K;
+    for (int64_t row = blockIdx.x; row < a.T + a.N; row += gridDim.x) {
+        const bool x = row < a.T;
+        const int64_t r = x ? row : row - a.T;
+        const int8_t* src = (x ? a.xq : a.wq) + r * K;
+        int8_t* dst = (x ? xp : wp) + r * Kp;
+        for (int k = threadIdx.x * 16; k < Kp; k += 256 * 16)
+            *reinterpret_cast<i32x4_t*>(dst + k) = k + 16 <= K ? load16(src + k) : load16_tail(src, k, K);
+    }
+}
+
 // ------------------------------------------------------------- choice of form
 
 // The tile forms, by what they cost: a workgroup's time per k-tile in ns where
@@ -720,15 +734,15 @@ constexpr int kRegsBig = kNumForms, kRegsSmall = kNumForms + 1;
 typedef Q8Tile<128, 128, 4, 1, 2, 3> FormR0;
 typedef Q8Tile<64, 64, 4, 2, 2, 4> FormR1;
 
-constexpr int kDirect = -1, kOneToken = -2;
+constexpr int kDirect = -1, kOneToken = -2, kPadded = -3;
 constexpr int kMaxParts = 16;
 
 struct Q8Plan {
-    int form;   // a tile form, kDirect or kOneToken
+    int form;   // a tile form, kDirect, kOneToken or kPadded
     int ks;     // parts of K
 };
 
-size_t plan_bytes(const Q8Plan& p, int64_t T, int64_t N) {
+size_t plan_bytes(const Q8Plan& p, int64_t T, int64_t N) {   // of a tile form
     if (p.ks == 1) return 0;
     const Q8Form& f = kForms[p.form];
     return (size_t)((T + f.bm - 1) / f.bm) * ((N + f.bn - 1) / f.bn) * f.bm * f.bn * sizeof(int) * p.ks;
@@ -763,21 +777,9 @@ int64_t cost_direct(int64_t T, int64_t N, int64_t K) {
     return 2500 + rounds * 16 * K * (420 + t * t) / 420 * 2 / 45;
 }
 
-Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
-    if (T == 1) return {kOneToken, 1};
-    if (K < 16) return {kDirect, 1};
-    if (!dma) {
-        // by rounds of 256 workgroups: 64 x 64 tiles cost 0.43 us a k-tile,
-        // 128 x 128 1.22 (1000 x 4099 x 4099: 70 us against 82; 1500 x 12001 x
-        // 4097: 270 against 217), and straight from memory 24 x 1025 x 5121
-        // takes 10 us, tiles 20
-        auto rounds = [&](int64_t b) { return (((T + b - 1) / b) * ((N + b - 1) / b) + 255) / 256; };
-        const int64_t nk = (K + 127) / 128, small = 5000 + rounds(64) * 430 * nk, big = 5000 + rounds(128) * 1220 * nk;
-        const int64_t direct = T <= 48 ? cost_direct(T, N, K) : INT64_MAX;
-        return {direct < small && direct < big ? kDirect : small <= big ? kRegsSmall : kRegsBig, 1};
-    }
-    Q8Plan best{kDirect, 1};
-    int64_t least = T <= 16 ? cost_direct(T, N, K) : INT64_MAX;
+// The tile form and parts of least cost.
+int64_t plan_tiles(int64_t T, int64_t N, int64_t K, Q8Plan& best) {
+    int64_t least = INT64_MAX;
     for (int f = 0; f < kNumForms; ++f)
         for (int ks = 1; ks <= kMaxParts && ks * 2 <= (K + 127) / 128 + 1; ++ks) {
             // parts are for tiles that leave CUs idle
@@ -788,7 +790,44 @@ Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
                 best = {f, ks};
             }
         }
-    return best;
+    return least;
+}
+
+int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
+
+Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
+    if (T == 1) return {kOneToken, 1};
+    if (K < 16) return {kDirect, 1};
+    Q8Plan best{kDirect, 1};
+    if (dma) return T <= 16 && cost_direct(T, N, K) <= plan_tiles(T, N, K, best) ? Q8Plan{kDirect, 1} : best;
+    // by rounds of 256 workgroups: 64 x 64 tiles cost 0.43 us a k-tile, 128 x
+    // 128 1.22 (1000 x 4099 x 4099: 70 us against 82; 1500 x 12001 x 4097: 270
+    // against 217), and straight from memory 24 x 1025 x 5121 takes 10 us,
+    // tiles 20.  Where d_in is no multiple of 4, rows padded to 16 bytes first
+    // cost a launch and their bytes once more (2000 x 4099 x 4099: 69 us against
+    // 128 through registers; 64 x 8193 x 8193: 30 against 44).
+    auto rounds = [&](int64_t b) { return (((T + b - 1) / b) * ((N + b - 1) / b) + 255) / 256; };
+    const int64_t nk = (K + 127) / 128, small = 5000 + rounds(64) * 430 * nk, big = 5000 + rounds(128) * 1220 * nk;
+    const int64_t direct = T <= 48 ? cost_direct(T, N, K) : INT64_MAX;
+    const int64_t pad = K % 4 == 0 ? INT64_MAX : 4500 + (T + N) * 2 * K / 4000 + plan_tiles(T, N, padded(K), best);
+    if (pad < direct && pad < small && pad < big) return {kPadded, 1};
+    return {direct < small && direct < big ? kDirect : small <= big ? kRegsSmall : kRegsBig, 1};
+}
+
+// Workspace of a padded product: x's rows, w's rows, and what their product needs.
+struct PadPlan {
+    Q8Plan plan;
+    size_t w, parts, bytes;   // offsets, and all
+};
+
+PadPlan plan_pad(int64_t T, int64_t N, int64_t K) {
+    PadPlan p;
+    const int64_t Kp = padded(K);
+    plan_tiles(T, N, Kp, p.plan);
+    p.w = align_up((size_t)(T * Kp), 256);
+    p.parts = p.w + align_up((size_t)(N * Kp), 256);
+    p.bytes = p.parts + plan_bytes(p.plan, T, N);
+    return p;
 }
 
 // ------------------------------------------------------------- launches
@@ -825,9 +864,7 @@ hipError_t launch_form(const MatmulQ8& a, int ks, void* workspace, hipStream_t s
 constexpr int64_t kPieceTokens = (int64_t)1 << 19;
 
 template <typename E>
-hipError_t launch_piece(const MatmulQ8& a, void* workspace, hipStream_t st) {
-    const bool dma = a.K % 4 == 0 && aligned_to(a.xq, 4) && aligned_to(a.wq, 4);
-    const Q8Plan p = plan_q8(a.T, a.N, a.K, dma);
+hipError_t launch_tiles(const MatmulQ8& a, const Q8Plan& p, void* workspace, hipStream_t st) {
     switch (p.form) {
         case 0: return launch_form<E, Form0>(a, p.ks, workspace, st);
         case 1: return launch_form<E, Form1>(a, p.ks, workspace, st);
@@ -836,8 +873,27 @@ hipError_t launch_piece(const MatmulQ8& a, void* workspace, hipStream_t st) {
         case 4: return launch_form<E, Form4>(a, p.ks, workspace, st);
         case 5: return launch_form<E, Form5>(a, p.ks, workspace, st);
         case kRegsBig: return launch_form<E, FormR0>(a, 1, workspace, st);
-        case kRegsSmall: return launch_form<E, FormR1>(a, 1, workspace, st);
-        default: break;
+        default: return launch_form<E, FormR1>(a, 1, workspace, st);
+    }
+}
+
+template <typename E>
+hipError_t launch_piece(const MatmulQ8& a, void* workspace, hipStream_t st) {
+    const bool dma = a.K % 4 == 0 && aligned_to(a.xq, 4) && aligned_to(a.wq, 4);
+    const Q8Plan p = plan_q8(a.T, a.N, a.K, dma);
+    if (p.form >= 0) return launch_tiles<E>(a, p, workspace, st);
+    if (p.form == kPadded) {
+        const PadPlan pad = plan_pad(a.T, a.N, a.K);
+        int8_t* ws = static_cast<int8_t*>(workspace);
+        MatmulQ8 b = a;
+        b.K = padded(a.K);
+        b.xq = ws;
+        b.wq = ws + pad.w;
+        const int64_t rows = a.T + a.N;
+        q8_pad<<<(unsigned)(rows < (1 << 20) ? rows : 1 << 20), 256, 0, st>>>(a, (int)b.K, ws, ws + pad.w);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        return launch_tiles<E>(b, pad.plan, ws + pad.parts, st);
     }
     if (p.form == kOneToken) {
         q8_one_token<E><<<(unsigned)((a.N + kRows - 1) / kRows), kWaves * 64, 0, st>>>(a);
@@ -869,13 +925,14 @@ hipError_t launch_typed(const MatmulQ8& a, void* workspace, hipStream_t st) {
 }  // namespace
 
 size_t matmul_q8_workspace_bytes(int64_t T, int64_t N, int64_t K) {
-    // the largest of the pieces'; only the forms of 4-byte aligned rows have
-    // parts, and whether codes are is known at the call
+    // the largest of the pieces'; of d_in that is a multiple of 4 only codes at
+    // 4-byte aligned addresses need any, which is known at the call
     size_t most = 0;
     const int64_t pieces[2] = {T < kPieceTokens ? T : kPieceTokens, T % kPieceTokens};
     for (int64_t t : pieces) {
-        if (t == 0 || K % 4 != 0) continue;
-        const size_t b = plan_bytes(plan_q8(t, N, K, true), t, N);
+        if (t == 0) continue;
+        const Q8Plan p = plan_q8(t, N, K, K % 4 == 0);
+        const size_t b = p.form == kPadded ? plan_pad(t, N, K).bytes : p.form >= 0 ? plan_bytes(p, t, N) : 0;
         most = b > most ? b : most;
     }
     return align_up(most, 256);

@@ -424,7 +424,8 @@ int dora_dequantize_rows(const int8_t* q, const float* scale, int64_t n, int64_t
  *   d_in          at most 131071, which no int32 sum of products can leave;
  *                 d_out at most 2^24 (beyond either: DORA_ERR_UNSUPPORTED).
  * Any alignment of the codes is accepted; rows that start at multiples of 4
- * bytes (d_in a multiple of 4) are read fastest.
+ * bytes (d_in a multiple of 4) are read fastest.  Others may be copied to the
+ * workspace first, which then holds both operands.
  * T == 0 is a no-op; T < 2^31.
  */
 int dora_matmul_q8(const int8_t* xq, const float* xscale, const int8_t* wq, const float* wscale, const float* bias,

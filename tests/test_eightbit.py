@@ -342,7 +342,7 @@ FORM_SIZES = [
     # and in parts
     (441, 5414, 8276), (134, 5554, 6244), (260, 3780, 5092), (70, 3273, 5676), (513, 2050, 8200), (75, 2113, 4332),
     (65, 884, 2064), (48, 512, 4100),
-    # rows that are not 4-byte aligned: 64 x 64 and 128 x 128 through registers
+    # rows that are not 4-byte aligned: through registers, or padded first
     (200, 900, 2049), (100, 129, 131), (2000, 1300, 1301), (1900, 2051, 130),
 ]
 
@@ -402,8 +402,9 @@ def test_matmul_q8_rows_do_not_depend_on_the_batch(N, K):
 
 def test_matmul_q8_misaligned_codes_and_in_place():
     say("[matmul_q8] misaligned codes; y over lora_out")
-    for T in (2, 40, 300):
-        y, (xq, xs, wq, ws, g, lora, b, s) = check_product(T, 260, 1024, "bf16", adapter=True)
+    # the last one through registers in 128 x 128 tiles
+    for T, N, K in ((1, 260, 1024), (2, 260, 1024), (40, 260, 1024), (300, 260, 1024), (2000, 1300, 1300)):
+        y, (xq, xs, wq, ws, g, lora, b, s) = check_product(T, N, K, "bf16", adapter=True)
         mis = D.matmul_q8(misaligned(xq), xs, misaligned(wq), ws, torch.bfloat16, g=g, lora_out=misaligned(lora), s=s,
                           out=misaligned(y))
         over = lora.clone()
