@@ -799,7 +799,10 @@ Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
     if (T == 1) return {kOneToken, 1};
     if (K < 16) return {kDirect, 1};
     Q8Plan best{kDirect, 1};
-    if (dma) return T <= 16 && cost_direct(T, N, K) <= plan_tiles(T, N, K, best) ? Q8Plan{kDirect, 1} : best;
+    if (dma) {
+        const int64_t tiles = plan_tiles(T, N, K, best);
+        return T <= 16 && cost_direct(T, N, K) <= tiles ? Q8Plan{kDirect, 1} : best;
+    }
     // by rounds of 256 workgroups: 64 x 64 tiles cost 0.43 us a k-tile, 128 x
     // 128 1.22 (1000 x 4099 x 4099: 70 us against 82; 1500 x 12001 x 4097: 270
     // against 217), and straight from memory 24 x 1025 x 5121 takes 10 us,
