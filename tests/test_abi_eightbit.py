@@ -95,6 +95,15 @@ def test_workspace_queries(lib):
         assert n.value <= 512 * 5120 * 4
 
 
+def test_workspaces_follow_the_forms():
+    # tiles that leave CUs idle are taken in parts, whose sums the workspace
+    # holds; a full chip and one token need none; odd rows are padded in it
+    assert D.matmul_q8_workspace_size(24, 5120, 5120) >= 2 * 24 * 5120 * 4
+    assert D.matmul_q8_workspace_size(333, 5120, 27648) >= 2 * 333 * 5120 * 4
+    assert D.matmul_q8_workspace_size(2048, 8192, 8192) == 0 and D.matmul_q8_workspace_size(1, 8192, 8191) == 0
+    assert (2000 + 4099) * 4099 <= D.matmul_q8_workspace_size(2000, 4099, 4099) <= (2000 + 4099 + 2) * 4112 + 512
+
+
 def test_a_small_workspace_is_refused(lib):
     need = ctypes.c_size_t()
     for T, N, K in ((64, 1024, 8192), (200, 1024, 8192), (333, 4090, 2056), (2048, 5120, 5120)):
