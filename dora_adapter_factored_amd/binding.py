@@ -132,22 +132,16 @@ def default_eps(dtype: torch.dtype) -> float:
 
 
 # ------------------------------------------------------------ workspaces
-_ws_cache: dict = {}
-
-
 def workspace(nbytes: int, device) -> torch.Tensor | None:
-    """A cached uint8 device buffer of at least nbytes for (device, current stream).
+    """A uint8 device buffer for one call, which holds it until it has launched.
 
-    Calls on one stream are ordered, so reusing the buffer across them is safe.
+    Every call has its own: it may launch several kernels, between which
+    another thread's call on the same stream may launch its own, and a captured
+    call's buffer has to outlive whatever is called after it.  It comes from
+    the caching allocator, where its memory is reused in the stream's order and
+    belongs to the graph's pool under capture.
     """
-    if nbytes == 0:
-        return None
-    key = (device, torch.cuda.current_stream(device).cuda_stream)
-    buf = _ws_cache.get(key)
-    if buf is None or buf.numel() < nbytes:
-        buf = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8, device=device)
-        _ws_cache[key] = buf
-    return buf
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
 def norm_workspace_size(d_out: int, d_in: int, r: int, dtype: torch.dtype) -> int:

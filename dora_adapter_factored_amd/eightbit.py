@@ -13,7 +13,7 @@ import functools
 
 import torch
 
-from .binding import _DTYPE_CODE, _check, _need, _ws_cache, load, workspace
+from .binding import _DTYPE_CODE, _check, _need, load, workspace
 
 _F32, _I8 = torch.float32, torch.int8
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -74,15 +74,9 @@ def matmul_q8_workspace_size(T: int, d_out: int, d_in: int) -> int:
     return n.value
 
 
-def _scratch(nbytes: int, ws, device):
-    """(pointer, bytes) of the caller's workspace, or of the cached one of this stream."""
-    if ws is None:
-        if nbytes == 0:
-            return None, 0
-        ws = _ws_cache.get((device, _stream(device)))   # workspace()'s own key
-        if ws is None or ws.numel() < nbytes:
-            ws = workspace(nbytes, device)
-    return ws.data_ptr(), ws.numel() * ws.element_size()
+def _extent(ws):
+    """(pointer, bytes) of a workspace, which the caller holds across its call."""
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 # ------------------------------------------------------------ norm
@@ -145,9 +139,11 @@ def rmsnorm_backward(dy, h, w, rstd, dh=None, *, need_dw: bool = True, dx=None, 
     dx = _out(dx, "dx", dev, dt, shape, dy)
     if need_dw:
         dw = _out(dw, "dw", dev, _F32, shape[1:])
-        wsp, nbytes = _scratch(rmsnorm_backward_workspace_size(T, d), ws, dev)
+        if ws is None:
+            ws = workspace(rmsnorm_backward_workspace_size(T, d), dev)
     else:
-        dw, wsp, nbytes = None, None, 0
+        dw = ws = None
+    wsp, nbytes = _extent(ws)
     st = load().dora_rmsnorm_backward(dy.data_ptr(), hp, wp, rp, dhp, T, d, _DTYPE_CODE[dt], dx.data_ptr(),
                                       None if dw is None else dw.data_ptr(), wsp, nbytes, _stream(dev))
     if st:
@@ -217,7 +213,9 @@ def matmul_q8(xq, xscale, wq, wscale=None, dtype: torch.dtype = torch.bfloat16, 
         gp = _in(g, "g", dev, _F32, (N,))
         lp = _in(lora_out, "lora_out", dev, dtype, (T, N))
     out = _out(out, "out", dev, dtype, (T, N))
-    wkp, nbytes = _scratch(matmul_q8_workspace_size(T, N, K), ws, dev)
+    if ws is None:
+        ws = workspace(matmul_q8_workspace_size(T, N, K), dev)
+    wkp, nbytes = _extent(ws)
     st = load().dora_matmul_q8(xq.data_ptr(), xsp, wp, wsp, bp, gp, lp, s, T, N, K, _DTYPE_CODE[dtype],
                                out.data_ptr(), wkp, nbytes, _stream(dev))
     if st:
@@ -225,20 +223,20 @@ def matmul_q8(xq, xscale, wq, wscale=None, dtype: torch.dtype = torch.bfloat16, 
     return out
 
 
-def linear_q8(x, wq, wscale, *, bias=None, g=None, lora_out=None, s: float = 1.0, out=None):
+def linear_q8(x, wq, wscale, *, bias=None, g=None, lora_out=None, s: float = 1.0, out=None, ws=None):
     """matmul_q8 of x [T, d_in], quantised by rows here; y has x's dtype."""
     xq, xscale = quantize_rows(x)
-    return matmul_q8(xq, xscale, wq, wscale, x.dtype, bias=bias, g=g, lora_out=lora_out, s=s, out=out)
+    return matmul_q8(xq, xscale, wq, wscale, x.dtype, bias=bias, g=g, lora_out=lora_out, s=s, out=out, ws=ws)
 
 
-def linear_q8_backward(dy, wqt, wscale, *, out=None):
+def linear_q8_backward(dy, wqt, wscale, *, out=None, ws=None):
     """d_x of the linear map x -> x (wscale wq)^T, with dy * wscale quantised by rows.
 
     wqt int8 [d_in, d_out] is wq transposed, laid out once:
     wq.t().contiguous().
     """
     dq, dscale = quantize_rows(dy, wscale)
-    return matmul_q8(dq, dscale, wqt, None, dy.dtype, out=out)
+    return matmul_q8(dq, dscale, wqt, None, dy.dtype, out=out, ws=ws)
 
 
 # ------------------------------------------------------------ autograd
