@@ -13,6 +13,7 @@ import os
 import threading
 
 import torch
+from torch.autograd.function import once_differentiable
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libdora_mi355x.so")
 
@@ -455,6 +456,7 @@ class DoRACompose(torch.autograd.Function):
         return compose(base_out, lora_out, g, s, delta_only)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         base_out, lora_out, g, wnorm = ctx.saved_tensors
         nb, nl, nm = ctx.need
@@ -481,6 +483,7 @@ class DoRAComposeInner(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         inner, g, wnorm = ctx.saved_tensors
         nb, nl, nm = ctx.need

@@ -12,6 +12,7 @@ import ctypes
 import functools
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .binding import _DTYPE_CODE, _check, _need, load, workspace
 
@@ -253,6 +254,7 @@ class RMSNorm(torch.autograd.Function):
         return (y, h) if ctx.has_residual else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dh=None):
         h, w, rstd = ctx.saved_tensors
         if dy is None:   # only h was used
@@ -273,6 +275,7 @@ class LinearQ8(torch.autograd.Function):
         return linear_q8(x, wq, wscale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         wqt, wscale = ctx.saved_tensors
         return linear_q8_backward(dy.contiguous(), wqt, wscale), None, None, None
