@@ -145,6 +145,14 @@ def workspace(nbytes: int, device) -> torch.Tensor | None:
     return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
 
 
+def _extent(ws, device):
+    """(pointer, bytes) of a workspace, the call's own or the caller's: the kernels write to it."""
+    if ws is None:
+        return None, 0
+    _need(ws, "ws", device)
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
 def norm_workspace_size(d_out: int, d_in: int, r: int, dtype: torch.dtype) -> int:
     n = ctypes.c_size_t(0)
     _check(load().dora_factored_norm_workspace_size(d_out, d_in, r, _DTYPE_CODE[dtype], ctypes.byref(n)),
@@ -207,9 +215,9 @@ def factored_norm(W0, A, B, s: float, m=None, eps: float | None = None, *, wnorm
         _need(g, "g", dev, torch.float32, (d_out,))
     if ws is None:
         ws = workspace(norm_workspace_size(d_out, d_in, r, W0.dtype), dev)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    wsp, nbytes = _extent(ws, dev)
     _check(lib.dora_factored_norm(_ptr(W0), _ptr(A), _ptr(B), _ptr(m), d_out, d_in, r, _DTYPE_CODE[W0.dtype],
-                                  float(s), eps, _ptr(wnorm), _ptr(g), _ptr(ws), nbytes, _stream(dev)),
+                                  float(s), eps, _ptr(wnorm), _ptr(g), wsp, nbytes, _stream(dev)),
            "dora_factored_norm")
     return wnorm, (g if m is not None else None)
 
@@ -286,8 +294,8 @@ def factored_norm_group(members, eps: float | None = None, *, outs=None, ws=None
     if ws is None:
         ws = workspace(norm_group_workspace_size([mb[0].shape[0] for mb in members],
                                                  [mb[0].shape[1] for mb in members], r, dt), dev)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib.dora_factored_norm_group(n, arr, r, _DTYPE_CODE[dt], eps, _ptr(ws), nbytes, _stream(dev)),
+    wsp, nbytes = _extent(ws, dev)
+    _check(lib.dora_factored_norm_group(n, arr, r, _DTYPE_CODE[dt], eps, wsp, nbytes, _stream(dev)),
            "dora_factored_norm_group")
     return results
 
@@ -312,9 +320,9 @@ def merge(W0, A, B, g, s: float, *, out=None, ws=None):
     _need(out, "out", dev, W0.dtype, (d_out, d_in))
     if ws is None:
         ws = workspace(merge_workspace_size(d_in, r, W0.dtype), dev)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    wsp, nbytes = _extent(ws, dev)
     _check(lib.dora_merge(_ptr(W0), _ptr(A), _ptr(B), _ptr(g), float(s), d_out, d_in, r, _DTYPE_CODE[W0.dtype],
-                          _ptr(out), _ptr(ws), nbytes, _stream(dev)),
+                          _ptr(out), wsp, nbytes, _stream(dev)),
            "dora_merge")
     return out
 
@@ -367,14 +375,14 @@ def compose_backward(dy, base_out, lora_out, g, wnorm, s: float, eps: float | No
         _need(d_m, "d_m", dev, torch.float32, (d_out,))
     if need_d_m and ws is None:
         ws = workspace(compose_backward_workspace_size(T, d_out), dev)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    wsp, nbytes = _extent(ws, dev)
     _check(lib.dora_compose_backward(_ptr(dy), _ptr(base_out) if need_d_m else None,
                                      _ptr(lora_out) if need_d_m else None, _ptr(g),
                                      _ptr(wnorm) if need_d_m else None, float(s), eps, T, d_out,
                                      _DTYPE_CODE[dy.dtype], int(bool(delta_only)),
                                      _ptr(d_base) if need_d_base else None,
                                      _ptr(d_lora) if need_d_lora else None,
-                                     _ptr(d_m) if need_d_m else None, _ptr(ws), nbytes, _stream(dev)),
+                                     _ptr(d_m) if need_d_m else None, wsp, nbytes, _stream(dev)),
            "dora_compose_backward")
     return (d_base if need_d_base else None, d_lora if need_d_lora else None, d_m if need_d_m else None)
 
@@ -430,13 +438,13 @@ def compose_backward_inner(dy, inner, g, wnorm, s: float, eps: float | None = No
         _need(d_m, "d_m", dev, torch.float32, (d_out,))
     if need_d_m and ws is None:
         ws = workspace(compose_backward_workspace_size(T, d_out), dev)
-    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    wsp, nbytes = _extent(ws, dev)
     _check(lib.dora_compose_backward_inner(_ptr(dy), _ptr(inner) if need_d_m else None, _ptr(g),
                                            _ptr(wnorm) if need_d_m else None, float(s), eps, T, d_out,
                                            _DTYPE_CODE[dy.dtype], int(bool(delta_only)),
                                            _ptr(d_base) if need_d_base else None,
                                            _ptr(d_lora) if need_d_lora else None,
-                                           _ptr(d_m) if need_d_m else None, _ptr(ws), nbytes, _stream(dev)),
+                                           _ptr(d_m) if need_d_m else None, wsp, nbytes, _stream(dev)),
            "dora_compose_backward_inner")
     return (d_base if need_d_base else None, d_lora if need_d_lora else None, d_m if need_d_m else None)
 

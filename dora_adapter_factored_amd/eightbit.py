@@ -14,7 +14,7 @@ import functools
 import torch
 from torch.autograd.function import once_differentiable
 
-from .binding import _DTYPE_CODE, _check, _need, load, workspace
+from .binding import _DTYPE_CODE, _check, _extent, _need, load, workspace
 
 _F32, _I8 = torch.float32, torch.int8
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -73,11 +73,6 @@ def matmul_q8_workspace_size(T: int, d_out: int, d_in: int) -> int:
     n = ctypes.c_size_t(0)
     _check(load().dora_matmul_q8_workspace_size(T, d_out, d_in, ctypes.byref(n)), "dora_matmul_q8_workspace_size")
     return n.value
-
-
-def _extent(ws):
-    """(pointer, bytes) of a workspace, which the caller holds across its call."""
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 # ------------------------------------------------------------ norm
@@ -144,7 +139,7 @@ def rmsnorm_backward(dy, h, w, rstd, dh=None, *, need_dw: bool = True, dx=None, 
             ws = workspace(rmsnorm_backward_workspace_size(T, d), dev)
     else:
         dw = ws = None
-    wsp, nbytes = _extent(ws)
+    wsp, nbytes = _extent(ws, dev)
     st = load().dora_rmsnorm_backward(dy.data_ptr(), hp, wp, rp, dhp, T, d, _DTYPE_CODE[dt], dx.data_ptr(),
                                       None if dw is None else dw.data_ptr(), wsp, nbytes, _stream(dev))
     if st:
@@ -216,7 +211,7 @@ def matmul_q8(xq, xscale, wq, wscale=None, dtype: torch.dtype = torch.bfloat16, 
     out = _out(out, "out", dev, dtype, (T, N))
     if ws is None:
         ws = workspace(matmul_q8_workspace_size(T, N, K), dev)
-    wkp, nbytes = _extent(ws)
+    wkp, nbytes = _extent(ws, dev)
     st = load().dora_matmul_q8(xq.data_ptr(), xsp, wp, wsp, bp, gp, lp, s, T, N, K, _DTYPE_CODE[dtype],
                                out.data_ptr(), wkp, nbytes, _stream(dev))
     if st:

@@ -92,6 +92,46 @@ def test_calls_in_flight_have_workspaces_of_their_own(monkeypatch, name, call, s
         assert hi <= seen[0][0] or seen[0][1] <= lo, "two calls in flight share a workspace"
 
 
+WITH_WS = [
+    ("dora_matmul_q8", lambda ws: D.matmul_q8(codes(24, 5120), f32(24), codes(5120, 5120), f32(5120), ws=ws)),
+    ("dora_matmul_q8", lambda ws: D.linear_q8(bf16(24, 5120), codes(5120, 5120), f32(5120), ws=ws)),
+    ("dora_matmul_q8", lambda ws: D.linear_q8_backward(bf16(24, 5120), codes(5120, 5120), f32(5120), ws=ws)),
+    ("dora_rmsnorm_backward", lambda ws: D.rmsnorm_backward(bf16(9, 64), bf16(9, 64), bf16(64), f32(9), ws=ws)),
+    ("dora_compose_backward", lambda ws: D.compose_backward(bf16(9, 64), bf16(9, 64), bf16(9, 64), f32(64), f32(64), 1.0, ws=ws)),
+    ("dora_compose_backward_inner", lambda ws: D.compose_backward_inner(bf16(9, 64), bf16(9, 64), f32(64), f32(64), 1.0, ws=ws)),
+    ("dora_factored_norm", lambda ws: D.factored_norm(bf16(64, 512), bf16(64, 512), bf16(64, 64), 1.0, ws=ws)),
+    ("dora_factored_norm_group", lambda ws: D.factored_norm_group([(bf16(64, 512), bf16(64, 512), bf16(64, 64), 1.0, None)], ws=ws)),
+    ("dora_merge", lambda ws: D.merge(bf16(64, 512), bf16(64, 512), bf16(64, 64), f32(64), 1.0, ws=ws)),
+]
+
+
+@pytest.mark.parametrize("name,call", WITH_WS, ids=[str(i) + c[0] for i, c in enumerate(WITH_WS)])
+def test_a_workspace_that_the_kernels_cannot_use_is_refused(monkeypatch, name, call):
+    # on another device than the operands, scattered or repeated in memory, or
+    # no tensor at all: before the call
+    real, reached = Bn.load(), []
+
+    class Stub:
+        def __getattr__(self, attr):
+            if attr.endswith("workspace_size"):
+                return getattr(real, attr)
+            return lambda *args: reached.append((attr, args[-2])) or 0
+
+    for mod in (Bn, E8):
+        monkeypatch.setattr(mod, "load", lambda: Stub())
+        monkeypatch.setattr(mod, "_stream", lambda device: 0)
+    n = 1 << 23
+    for bad in (torch.empty(n, dtype=torch.uint8, device="meta"), torch.empty(1, dtype=torch.uint8).expand(n),
+                torch.empty(2 * n, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="ws"):
+            call(bad)
+    with pytest.raises(TypeError, match="ws"):
+        call(1 << 20)
+    assert not [a for a, _ in reached if a == name]
+    call(torch.empty(n // 4))   # any element type
+    assert (name, n) in reached
+
+
 # ------------------------------------------------------------------ on the GPU
 DEV = torch.device("cuda:0")
 
