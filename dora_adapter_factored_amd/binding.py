@@ -106,6 +106,25 @@ def _check(status: int, where: str):
         raise DoraError(status, where)
 
 
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(name: str, device, *args):
+    """The entry point on its operands' GPU, which need not be the current one.
+
+    The library launches on the current device, and the default stream's handle
+    is the same on all of them.
+    """
+    fn = getattr(load(), name)
+    if device.index is None or device.index == _current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st:
+        _check(st, name)
+
+
 def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -194,7 +213,6 @@ def factored_norm(W0, A, B, s: float, m=None, eps: float | None = None, *, wnorm
     W0 [d_out, d_in], A [r, d_in], B [d_out, r] share a dtype (bf16 or fp32);
     m is fp32 [d_out] or None.  Returns (wnorm, g) with g None when m is None.
     """
-    lib = load()
     dev = W0.device
     d_out, d_in = W0.shape
     r = A.shape[0]
@@ -216,9 +234,8 @@ def factored_norm(W0, A, B, s: float, m=None, eps: float | None = None, *, wnorm
     if ws is None:
         ws = workspace(norm_workspace_size(d_out, d_in, r, W0.dtype), dev)
     wsp, nbytes = _extent(ws, dev)
-    _check(lib.dora_factored_norm(_ptr(W0), _ptr(A), _ptr(B), _ptr(m), d_out, d_in, r, _DTYPE_CODE[W0.dtype],
-                                  float(s), eps, _ptr(wnorm), _ptr(g), wsp, nbytes, _stream(dev)),
-           "dora_factored_norm")
+    _call("dora_factored_norm", dev, _ptr(W0), _ptr(A), _ptr(B), _ptr(m), d_out, d_in, r, _DTYPE_CODE[W0.dtype],
+          float(s), eps, _ptr(wnorm), _ptr(g), wsp, nbytes, _stream(dev))
     return wnorm, (g if m is not None else None)
 
 
@@ -226,7 +243,6 @@ def factored_norm_noalloc(W0, A, B, s: float, m=None, eps: float | None = None, 
     """factored_norm through dora_factored_norm_noalloc: no workspace, the
     library's static per-GPU scratch instead (same kernels, bitwise the same
     result).  Outputs are allocated here unless given."""
-    lib = load()
     dev = W0.device
     d_out, d_in = W0.shape
     r = A.shape[0]
@@ -246,10 +262,8 @@ def factored_norm_noalloc(W0, A, B, s: float, m=None, eps: float | None = None, 
     if g is not None:
         _need(g, "g", dev, torch.float32, (d_out,))
     with torch.cuda.device(dev):
-        _check(lib.dora_factored_norm_noalloc(_ptr(W0), _ptr(A), _ptr(B), _ptr(m), d_out, d_in, r,
-                                              _DTYPE_CODE[W0.dtype], float(s), eps, _ptr(wnorm), _ptr(g),
-                                              _stream(dev)),
-               "dora_factored_norm_noalloc")
+        _call("dora_factored_norm_noalloc", dev, _ptr(W0), _ptr(A), _ptr(B), _ptr(m), d_out, d_in, r,
+              _DTYPE_CODE[W0.dtype], float(s), eps, _ptr(wnorm), _ptr(g), _stream(dev))
     return wnorm, (g if m is not None else None)
 
 
@@ -261,7 +275,6 @@ def factored_norm_group(members, eps: float | None = None, *, outs=None, ws=None
     member, g None where m is None; each equals factored_norm's result for
     that member bitwise.
     """
-    lib = load()
     n = len(members)
     if not 1 <= n <= MAX_NORM_GROUP:
         raise ValueError(f"a group holds 1..{MAX_NORM_GROUP} members (got {n})")
@@ -295,8 +308,7 @@ def factored_norm_group(members, eps: float | None = None, *, outs=None, ws=None
         ws = workspace(norm_group_workspace_size([mb[0].shape[0] for mb in members],
                                                  [mb[0].shape[1] for mb in members], r, dt), dev)
     wsp, nbytes = _extent(ws, dev)
-    _check(lib.dora_factored_norm_group(n, arr, r, _DTYPE_CODE[dt], eps, wsp, nbytes, _stream(dev)),
-           "dora_factored_norm_group")
+    _call("dora_factored_norm_group", dev, n, arr, r, _DTYPE_CODE[dt], eps, wsp, nbytes, _stream(dev))
     return results
 
 
@@ -305,7 +317,6 @@ def merge(W0, A, B, g, s: float, *, out=None, ws=None):
 
     g is fp32 [d_out] (the g of factored_norm).  out=W0 merges in place.
     """
-    lib = load()
     dev = W0.device
     d_out, d_in = W0.shape
     r = A.shape[0]
@@ -321,15 +332,13 @@ def merge(W0, A, B, g, s: float, *, out=None, ws=None):
     if ws is None:
         ws = workspace(merge_workspace_size(d_in, r, W0.dtype), dev)
     wsp, nbytes = _extent(ws, dev)
-    _check(lib.dora_merge(_ptr(W0), _ptr(A), _ptr(B), _ptr(g), float(s), d_out, d_in, r, _DTYPE_CODE[W0.dtype],
-                          _ptr(out), wsp, nbytes, _stream(dev)),
-           "dora_merge")
+    _call("dora_merge", dev, _ptr(W0), _ptr(A), _ptr(B), _ptr(g), float(s), d_out, d_in, r, _DTYPE_CODE[W0.dtype],
+          _ptr(out), wsp, nbytes, _stream(dev))
     return out
 
 
 def compose(base_out, lora_out, g, s: float, delta_only: bool = False, *, out=None):
     """y = base + ((g-1)*base + (g*s)*lora) (or the delta alone), one fused pass."""
-    lib = load()
     dev = base_out.device
     T, d_out = base_out.shape
     _need(base_out, "base_out", dev)
@@ -340,9 +349,8 @@ def compose(base_out, lora_out, g, s: float, delta_only: bool = False, *, out=No
     if out is None:
         out = torch.empty_like(base_out)
     _need(out, "out", dev, base_out.dtype, (T, d_out))
-    _check(lib.dora_compose(_ptr(base_out), _ptr(lora_out), _ptr(g), float(s), T, d_out,
-                            _DTYPE_CODE[base_out.dtype], int(bool(delta_only)), _ptr(out), _stream(dev)),
-           "dora_compose")
+    _call("dora_compose", dev, _ptr(base_out), _ptr(lora_out), _ptr(g), float(s), T, d_out, _DTYPE_CODE[base_out.dtype],
+          int(bool(delta_only)), _ptr(out), _stream(dev))
     return out
 
 
@@ -350,7 +358,6 @@ def compose_backward(dy, base_out, lora_out, g, wnorm, s: float, eps: float | No
                      delta_only: bool = False, *, need_d_base=True, need_d_lora=True, need_d_m=True,
                      d_base=None, d_lora=None, d_m=None, ws=None):
     """(d_base, d_lora, d_m) of compose with the norm detached; unrequested ones are None."""
-    lib = load()
     dev = dy.device
     T, d_out = dy.shape
     _need(dy, "dy", dev)
@@ -376,20 +383,15 @@ def compose_backward(dy, base_out, lora_out, g, wnorm, s: float, eps: float | No
     if need_d_m and ws is None:
         ws = workspace(compose_backward_workspace_size(T, d_out), dev)
     wsp, nbytes = _extent(ws, dev)
-    _check(lib.dora_compose_backward(_ptr(dy), _ptr(base_out) if need_d_m else None,
-                                     _ptr(lora_out) if need_d_m else None, _ptr(g),
-                                     _ptr(wnorm) if need_d_m else None, float(s), eps, T, d_out,
-                                     _DTYPE_CODE[dy.dtype], int(bool(delta_only)),
-                                     _ptr(d_base) if need_d_base else None,
-                                     _ptr(d_lora) if need_d_lora else None,
-                                     _ptr(d_m) if need_d_m else None, wsp, nbytes, _stream(dev)),
-           "dora_compose_backward")
+    _call("dora_compose_backward", dev, _ptr(dy), _ptr(base_out) if need_d_m else None,
+          _ptr(lora_out) if need_d_m else None, _ptr(g), _ptr(wnorm) if need_d_m else None, float(s), eps, T, d_out,
+          _DTYPE_CODE[dy.dtype], int(bool(delta_only)), _ptr(d_base) if need_d_base else None,
+          _ptr(d_lora) if need_d_lora else None, _ptr(d_m) if need_d_m else None, wsp, nbytes, _stream(dev))
     return (d_base if need_d_base else None, d_lora if need_d_lora else None, d_m if need_d_m else None)
 
 
 def compose_dual(base_out, lora_out, g, s: float, delta_only: bool = False, *, out=None, inner=None):
     """(y, inner): the compose output and inner = base + s*lora from one pass."""
-    lib = load()
     dev = base_out.device
     T, d_out = base_out.shape
     _need(base_out, "base_out", dev)
@@ -403,10 +405,8 @@ def compose_dual(base_out, lora_out, g, s: float, delta_only: bool = False, *, o
         inner = torch.empty_like(base_out)
     _need(out, "out", dev, base_out.dtype, (T, d_out))
     _need(inner, "inner", dev, base_out.dtype, (T, d_out))
-    _check(lib.dora_compose_dual(_ptr(base_out), _ptr(lora_out), _ptr(g), float(s), T, d_out,
-                                 _DTYPE_CODE[base_out.dtype], int(bool(delta_only)), _ptr(out), _ptr(inner),
-                                 _stream(dev)),
-           "dora_compose_dual")
+    _call("dora_compose_dual", dev, _ptr(base_out), _ptr(lora_out), _ptr(g), float(s), T, d_out,
+          _DTYPE_CODE[base_out.dtype], int(bool(delta_only)), _ptr(out), _ptr(inner), _stream(dev))
     return out, inner
 
 
@@ -414,7 +414,6 @@ def compose_backward_inner(dy, inner, g, wnorm, s: float, eps: float | None = No
                            need_d_base=True, need_d_lora=True, need_d_m=True, d_base=None, d_lora=None, d_m=None,
                            ws=None):
     """(d_base, d_lora, d_m) from (dy, inner) with the norm detached; unrequested ones are None."""
-    lib = load()
     dev = dy.device
     T, d_out = dy.shape
     _need(dy, "dy", dev)
@@ -439,13 +438,10 @@ def compose_backward_inner(dy, inner, g, wnorm, s: float, eps: float | None = No
     if need_d_m and ws is None:
         ws = workspace(compose_backward_workspace_size(T, d_out), dev)
     wsp, nbytes = _extent(ws, dev)
-    _check(lib.dora_compose_backward_inner(_ptr(dy), _ptr(inner) if need_d_m else None, _ptr(g),
-                                           _ptr(wnorm) if need_d_m else None, float(s), eps, T, d_out,
-                                           _DTYPE_CODE[dy.dtype], int(bool(delta_only)),
-                                           _ptr(d_base) if need_d_base else None,
-                                           _ptr(d_lora) if need_d_lora else None,
-                                           _ptr(d_m) if need_d_m else None, wsp, nbytes, _stream(dev)),
-           "dora_compose_backward_inner")
+    _call("dora_compose_backward_inner", dev, _ptr(dy), _ptr(inner) if need_d_m else None, _ptr(g),
+          _ptr(wnorm) if need_d_m else None, float(s), eps, T, d_out, _DTYPE_CODE[dy.dtype], int(bool(delta_only)),
+          _ptr(d_base) if need_d_base else None, _ptr(d_lora) if need_d_lora else None, _ptr(d_m) if need_d_m else None,
+          wsp, nbytes, _stream(dev))
     return (d_base if need_d_base else None, d_lora if need_d_lora else None, d_m if need_d_m else None)
 
 

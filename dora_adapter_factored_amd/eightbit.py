@@ -14,7 +14,7 @@ import functools
 import torch
 from torch.autograd.function import once_differentiable
 
-from .binding import _DTYPE_CODE, _check, _extent, _need, load, workspace
+from .binding import _DTYPE_CODE, _call, _check, _extent, _need, load, workspace
 
 _F32, _I8 = torch.float32, torch.int8
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -86,12 +86,9 @@ def _norm(x, w, eps, residual, h, dev, dt, shape, y, q, scale, rstd):
         hp = h.data_ptr()
     elif h is not None:
         raise ValueError("h is an output of the addition: it needs a residual")
-    st = load().dora_rmsnorm(x.data_ptr(), rp, wp, eps, shape[0], shape[1], _DTYPE_CODE[dt], hp,
-                             None if y is None else y.data_ptr(), None if q is None else q.data_ptr(),
-                             None if scale is None else scale.data_ptr(), None if rstd is None else rstd.data_ptr(),
-                             _stream(dev))
-    if st:
-        _check(st, "dora_rmsnorm")
+    _call("dora_rmsnorm", dev, x.data_ptr(), rp, wp, eps, shape[0], shape[1], _DTYPE_CODE[dt], hp,
+          None if y is None else y.data_ptr(), None if q is None else q.data_ptr(),
+          None if scale is None else scale.data_ptr(), None if rstd is None else rstd.data_ptr(), _stream(dev))
     return x if residual is None else h
 
 
@@ -140,10 +137,8 @@ def rmsnorm_backward(dy, h, w, rstd, dh=None, *, need_dw: bool = True, dx=None, 
     else:
         dw = ws = None
     wsp, nbytes = _extent(ws, dev)
-    st = load().dora_rmsnorm_backward(dy.data_ptr(), hp, wp, rp, dhp, T, d, _DTYPE_CODE[dt], dx.data_ptr(),
-                                      None if dw is None else dw.data_ptr(), wsp, nbytes, _stream(dev))
-    if st:
-        _check(st, "dora_rmsnorm_backward")
+    _call("dora_rmsnorm_backward", dev, dy.data_ptr(), hp, wp, rp, dhp, T, d, _DTYPE_CODE[dt], dx.data_ptr(),
+          None if dw is None else dw.data_ptr(), wsp, nbytes, _stream(dev))
     return dx, dw
 
 
@@ -154,10 +149,8 @@ def quantize_rows(x, col_scale=None, *, q=None, scale=None):
     cp = None if col_scale is None else _in(col_scale, "col_scale", dev, _F32, shape[1:])
     q = _out(q, "q", dev, _I8, shape)
     scale = _out(scale, "scale", dev, _F32, shape[:1])
-    st = load().dora_quantize_rows(x.data_ptr(), cp, shape[0], shape[1], _DTYPE_CODE[dt], q.data_ptr(),
-                                   scale.data_ptr(), _stream(dev))
-    if st:
-        _check(st, "dora_quantize_rows")
+    _call("dora_quantize_rows", dev, x.data_ptr(), cp, shape[0], shape[1], _DTYPE_CODE[dt], q.data_ptr(),
+          scale.data_ptr(), _stream(dev))
     return q, scale
 
 
@@ -168,10 +161,8 @@ def dequantize_rows(q, scale, dtype: torch.dtype, *, out=None):
         raise ValueError(f"unsupported dtype {dtype}")
     sp = _in(scale, "scale", dev, _F32, shape[:1])
     out = _out(out, "out", dev, dtype, shape)
-    st = load().dora_dequantize_rows(q.data_ptr(), sp, shape[0], shape[1], _DTYPE_CODE[dtype], out.data_ptr(),
-                                     _stream(dev))
-    if st:
-        _check(st, "dora_dequantize_rows")
+    _call("dora_dequantize_rows", dev, q.data_ptr(), sp, shape[0], shape[1], _DTYPE_CODE[dtype], out.data_ptr(),
+          _stream(dev))
     return out
 
 
@@ -212,10 +203,8 @@ def matmul_q8(xq, xscale, wq, wscale=None, dtype: torch.dtype = torch.bfloat16, 
     if ws is None:
         ws = workspace(matmul_q8_workspace_size(T, N, K), dev)
     wkp, nbytes = _extent(ws, dev)
-    st = load().dora_matmul_q8(xq.data_ptr(), xsp, wp, wsp, bp, gp, lp, s, T, N, K, _DTYPE_CODE[dtype],
-                               out.data_ptr(), wkp, nbytes, _stream(dev))
-    if st:
-        _check(st, "dora_matmul_q8")
+    _call("dora_matmul_q8", dev, xq.data_ptr(), xsp, wp, wsp, bp, gp, lp, s, T, N, K, _DTYPE_CODE[dtype],
+          out.data_ptr(), wkp, nbytes, _stream(dev))
     return out
 
 
