@@ -25,22 +25,23 @@ EPS = 1e-6
 
 
 def projection(d_out, d_in, r, seed, dev):
-    """A frozen projection with a DoRA adapter: its layer, g and wnorm."""
-    L = DI.make_layer(DI.custom_spec(d_out, d_in, r, 1, dtype="bf16", s=2.0, b_std=0.02, m_noise=0.05), seed, device=dev,
-                      activations=False, gen_device=dev)
-    wnorm, g = D.factored_norm(L.W0, L.A, L.B, L.spec.s, L.m)
-    return L, wnorm, g
+    """A frozen projection with a DoRA adapter."""
+    return DI.make_layer(DI.custom_spec(d_out, d_in, r, 1, dtype="bf16", s=2.0, b_std=0.02, m_noise=0.05), seed, device=dev,
+                         activations=False, gen_device=dev)
 
 
 class Block:
     def __init__(self, hidden, inner, r, dev):
-        self.up, self.up_wnorm, self.up_g = projection(inner, hidden, r, 1, dev)
-        self.down, _, down_g = projection(hidden, inner, r, 2, dev)
+        self.up, self.down = projection(inner, hidden, r, 1, dev), projection(hidden, inner, r, 2, dev)
         self.norm_w = torch.ones(hidden, dtype=torch.bfloat16, device=dev)
         # 8-bit weights, laid out once: W0 with the adapter beside it, the other merged
         self.up_q, self.up_s = D.quantize_rows(self.up.W0)
         self.up_qt = self.up_q.t().contiguous()
-        self.down_q, self.down_s = D.quantize_rows(D.merge(self.down.W0, self.down.A, self.down.B, down_g, self.down.spec.s))
+        # the norm of the weight that the product computes with, which is the one in 8 bits
+        W8 = D.dequantize_rows(self.up_q, self.up_s, torch.float32)
+        self.up_wnorm, self.up_g = D.factored_norm(W8, self.up.A.float(), self.up.B.float(), self.up.spec.s, self.up.m)
+        _, g = D.factored_norm(self.down.W0, self.down.A, self.down.B, self.down.spec.s, self.down.m)
+        self.down_q, self.down_s = D.quantize_rows(D.merge(self.down.W0, self.down.A, self.down.B, g, self.down.spec.s))
 
     def serve(self, x, residual):
         """(output, new residual) for the tokens x [T, hidden]."""
