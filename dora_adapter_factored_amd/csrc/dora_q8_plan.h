@@ -41,11 +41,11 @@ inline size_t plan_bytes(const Q8Plan& p, int64_t T, int64_t N) {   // of a tile
 // k-tiles; a launch about 5 us, of which the loads' first latency and the
 // epilogue are most; parts that have to be joined one more launch (3 us, and
 // for a short call as much again on the host: 4.5) and their bytes written and
-// read again (0.23 us for each MB).  At 333 x 5120 x
-// 27648 this takes 128 x 256 tiles in 4 parts (67 us; without parts 88), at
-// 2048 x 5120 x 5120 192 x 256 tiles (58.5 us; 256 x 256 65.4, 128 x 256
-// 80.9), at 512 x 8192 x 8192 128 x 128 (42.1 us; 128 x 256 54.9, 64 x 128
-// 54.4).
+// read again (0.23 us for each MB).  At 333 x 5120 x 27648 this takes 192 x 256
+// tiles in 6 parts (73 us; 128 x 256 in 4 69, every form without parts over
+// 92), at 2048 x 5120 x 5120 192 x 256 tiles (58 us; 256 x 256 67, 128 x 256
+// 81), at 512 x 8192 x 8192 128 x 128 (45 us; 128 x 256 in 2 parts 49, 64 x 128
+// 55).
 inline int64_t cost_q8(int form, int ks, int64_t T, int64_t N, int64_t K) {
     const Q8Form& f = kForms[form];
     const int64_t wgs = ((T + f.bm - 1) / f.bm) * ((N + f.bn - 1) / f.bn) * ks, nk = ((K + 127) / 128 + ks - 1) / ks;
@@ -64,6 +64,13 @@ inline int64_t cost_q8(int form, int ks, int64_t T, int64_t N, int64_t K) {
 inline int64_t cost_direct(int64_t T, int64_t N, int64_t K) {
     const int64_t rounds = ((N + 15) / 16 * ((T + 15) / 16) + 255) / 256, t = T < 16 ? T : 16;
     return 2500 + rounds * 16 * K * (420 + t * t) / 420 * 2 / 45;
+}
+
+// The same for rows that are not 4-byte aligned, by whole dwords: 13.3 GB/s a
+// CU at one token, 9.1 at 16.
+inline int64_t cost_direct_odd(int64_t T, int64_t N, int64_t K) {
+    const int64_t rounds = ((N + 15) / 16 * ((T + 15) / 16) + 255) / 256, t = T < 16 ? T : 16;
+    return 2500 + rounds * 16 * K * (28 + t) / 400;
 }
 
 // The tile form and parts of least cost.
@@ -94,16 +101,22 @@ inline Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
         const int64_t tiles = plan_tiles(T, N, K, best);
         return T <= 16 && cost_direct(T, N, K) <= tiles ? Q8Plan{kDirect, 1} : best;
     }
-    // by rounds of 256 workgroups: 64 x 64 tiles cost 0.43 us a k-tile, 128 x
-    // 128 1.22 (1000 x 4099 x 4099: 70 us against 82; 1500 x 12001 x 4097: 270
-    // against 217), and straight from memory 24 x 1025 x 5121 takes 10 us,
-    // tiles 20.  Where d_in is no multiple of 4, rows padded to 16 bytes first
-    // cost a launch and their bytes once more (2000 x 4099 x 4099: 69 us against
-    // 128 through registers; 64 x 8193 x 8193: 30 against 44).
+    // Rows that are not 4-byte aligned, by rounds of 256 workgroups: 64 x 64
+    // tiles through registers cost 0.43 us a k-tile, 128 x 128 1.22.  Up to 64
+    // tokens may go straight from memory.  Where d_in is no multiple of 4, rows
+    // may be padded to 16 bytes first, for a launch and their bytes both ways
+    // (written at 5.3 TB/s, and read again in part from the MALL).  Measured, GPU
+    // time with weights that are not in the MALL, straight / padded / 64 x 64 /
+    // 128 x 128 in us: 24 x 5120 x 27649 149 / 80 / 98 / 210, 64 x 300 x 1001
+    // 4.3 / 9.2 / 8.8 / 16, 64 x 4099 x 4099 30 / 21 / 19 / 36, 64 x 8193 x 8193
+    // 113 / 45 / 45 / 81, 333 x 8193 x 8193 - / 71 / 116 / 86, 1000 x 515 x 16385
+    // - / 35 / 54 / 128, 100 x 28673 x 2049 - / 46 / 46 / 34, 2000 x 4099 x 4099
+    // - / 68 / 128 / 121.  Over 266 such sizes the form that this takes is 0.4% slower
+    // than the fastest one in the mean, and 18% at most.
     auto rounds = [&](int64_t b) { return (((T + b - 1) / b) * ((N + b - 1) / b) + 255) / 256; };
     const int64_t nk = (K + 127) / 128, small = 5000 + rounds(64) * 430 * nk, big = 5000 + rounds(128) * 1220 * nk;
-    const int64_t direct = T <= 48 ? cost_direct(T, N, K) : INT64_MAX;
-    const int64_t pad = K % 4 == 0 ? INT64_MAX : 4500 + (T + N) * 2 * K / 4000 + plan_tiles(T, N, padded(K), best);
+    const int64_t direct = T <= 64 ? cost_direct_odd(T, N, K) : INT64_MAX;
+    const int64_t pad = K % 4 == 0 ? INT64_MAX : 4500 + (T + N) * 2 * K / 6000 + plan_tiles(T, N, padded(K), best);
     if (pad < direct && pad < small && pad < big) return {kPadded, 1};
     return {direct < small && direct < big ? kDirect : small <= big ? kRegsSmall : kRegsBig, 1};
 }
