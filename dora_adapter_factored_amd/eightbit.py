@@ -75,6 +75,14 @@ def matmul_q8_workspace_size(T: int, d_out: int, d_in: int) -> int:
     return n.value
 
 
+def _scratch(ws, nbytes: int, device):
+    """(buffer, pointer, bytes): the caller's workspace or the call's own, which the call holds."""
+    if ws is not None:
+        return (ws, *_extent(ws, device))
+    ws = workspace(nbytes, device)
+    return ws, None if ws is None else ws.data_ptr(), nbytes
+
+
 # ------------------------------------------------------------ norm
 def _norm(x, w, eps, residual, h, dev, dt, shape, y, q, scale, rstd):
     """The call, and h: x itself where there is no residual."""
@@ -132,11 +140,9 @@ def rmsnorm_backward(dy, h, w, rstd, dh=None, *, need_dw: bool = True, dx=None, 
     dx = _out(dx, "dx", dev, dt, shape, dy)
     if need_dw:
         dw = _out(dw, "dw", dev, _F32, shape[1:])
-        if ws is None:
-            ws = workspace(rmsnorm_backward_workspace_size(T, d), dev)
+        ws, wsp, nbytes = _scratch(ws, rmsnorm_backward_workspace_size(T, d), dev)
     else:
-        dw = ws = None
-    wsp, nbytes = _extent(ws, dev)
+        dw, wsp, nbytes = None, None, 0
     _call("dora_rmsnorm_backward", dev, dy.data_ptr(), hp, wp, rp, dhp, T, d, _DTYPE_CODE[dt], dx.data_ptr(),
           None if dw is None else dw.data_ptr(), wsp, nbytes, _stream(dev))
     return dx, dw
@@ -200,9 +206,7 @@ def matmul_q8(xq, xscale, wq, wscale=None, dtype: torch.dtype = torch.bfloat16, 
         gp = _in(g, "g", dev, _F32, (N,))
         lp = _in(lora_out, "lora_out", dev, dtype, (T, N))
     out = _out(out, "out", dev, dtype, (T, N))
-    if ws is None:
-        ws = workspace(matmul_q8_workspace_size(T, N, K), dev)
-    wkp, nbytes = _extent(ws, dev)
+    ws, wkp, nbytes = _scratch(ws, matmul_q8_workspace_size(T, N, K), dev)
     _call("dora_matmul_q8", dev, xq.data_ptr(), xsp, wp, wsp, bp, gp, lp, s, T, N, K, _DTYPE_CODE[dtype],
           out.data_ptr(), wkp, nbytes, _stream(dev))
     return out
