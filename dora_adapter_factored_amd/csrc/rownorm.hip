@@ -4,7 +4,7 @@
 //
 // Forward, row t of [T, d], all in fp32, each output rounded once:
 //   h = x + residual,  rstd = 1 / sqrt(mean_j h_j^2 + eps),  y = h rstd w
-//   scale = max_j |y_j| / 127,  q_j = rint(y_j / scale)
+//   scale = max_j |y_j| fl(1/127),  q_j = rint(y_j / scale)
 // The codes are those of the fp32 y, with the division rounded as IEEE has it:
 // an outlier channel makes a code's step a large part of a row's rms, and a
 // code that falls the other way at a tie is seen.  (One reduction would do, as
@@ -104,7 +104,8 @@ __device__ __forceinline__ Divisor divisor(float scale) {
 // rounding or two, which rint takes back to 127.  The quotient is Markstein's:
 // p times the reciprocal, corrected by its remainder, which is p / scale
 // correctly rounded (a division for each element took 22.6 us at 4096 x 8192
-// where this takes 18).
+// where this takes 18).  Below a largest |p| of 2^-94 the remainder may
+// underflow, and a code next to a tie be the other one.
 template <bool AL, int N>
 __device__ __forceinline__ void store_codes(int8_t* q, const float (&p)[N], const Divisor& by, int64_t left) {
     int c[N];
@@ -156,8 +157,12 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
 // |v|'s bits, whose order as integers is the values', NaN above infinity.
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
-// A row's scale from the bits of its largest |value|.  A row that holds a NaN
-// or an infinity has scale NaN (and codes 0), so all that comes of it is NaN.
+// A row's scale from the bits of its largest |value|: times fl(1/127), which is
+// the quotient by 127 but for its last bit in 4.5% of values.  The codes are
+// exact for the scale as it is stored; a division would change those of weights
+// that are kept (torch's amax / 127 on the GPU is this product too).  A row that
+// holds a NaN or an infinity has scale NaN (and codes 0), so all that comes of it
+// is NaN.
 __device__ __forceinline__ float code_scale(uint32_t top) {
     return top >= kInfBits ? __uint_as_float(0x7fc00000u) : top < kTinyBits ? 0.0f : __uint_as_float(top) * (1.0f / 127.0f);
 }

@@ -321,8 +321,13 @@ int dora_merge(const void* W0, const void* A, const void* B, const float* g, flo
  *
  * A weight held in 8 bits is a matrix of signed codes in [-127, 127] with one
  * fp32 scale per row (output channel); an activation in 8 bits is the same
- * with one scale per token.  A code stands for code * scale.  Rounding is to
- * nearest even and symmetric: scale = (largest |value| of the row) / 127.
+ * with one scale per token.  A code stands for code * scale.  In fp32:
+ *   scale = (largest |value| of the row) * c, c the fp32 number nearest 1/127:
+ *           one product, within a unit in the last place of the quotient by 127
+ *   code  = value / scale, that quotient rounded to fp32, then to the nearest
+ *           integer, ties to even
+ * (rows whose largest |value| is below 2^-94 may have the other code where the
+ * quotient is within a rounding of a tie).
  *   - A row of zeros has scale 0 and codes 0; so has one whose largest |value|
  *     is below 2^-119.
  *   - A row that holds a NaN or an infinity has scale NaN and codes 0, so that
