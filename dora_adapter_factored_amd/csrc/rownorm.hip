@@ -532,7 +532,13 @@ __global__ __launch_bounds__(256) void dequantize(const int8_t* __restrict__ q, 
             }
             float v[N];
 #pragma unroll
-            for (int e = 0; e < N; ++e) v[e] = (float)c[e] * s;
+            for (int e = 0; e < N; ++e) {
+                v[e] = (float)c[e] * s;
+                // the product as it is in fp32: in fp16 the compiler otherwise
+                // joins it with its conversion where rows are not aligned, and
+                // not where they are, and the two round differently
+                asm volatile("" : "+v"(v[e]));
+            }
             store_row<E, AL>(out + row * d + k * N, v, left);
         }
     }

@@ -402,8 +402,8 @@ int dora_quantize_rows(const void* x, const float* col_scale, int64_t n, int64_t
                        void* stream);
 
 /*
- * out = q * scale by rows, rounded once to dtype: for operators that take the
- * weight itself, such as dora_factored_norm.
+ * out = the fp32 product q * scale by rows, rounded to dtype: for operators that
+ * take the weight itself, such as dora_factored_norm.
  */
 int dora_dequantize_rows(const int8_t* q, const float* scale, int64_t n, int64_t d, int dtype, void* out, void* stream);
 
