@@ -93,7 +93,7 @@ inline int64_t padded(int64_t K) { return (K + 15) / 16 * 16; }
 
 inline size_t round_up_256(size_t x) { return (x + 255) / 256 * 256; }
 
-inline Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
+inline Q8Plan make_plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
     if (T == 1) return {kOneToken, 1};
     if (K < 16) return {kDirect, 1};
     Q8Plan best{kDirect, 1};
@@ -119,6 +119,19 @@ inline Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
     const int64_t pad = K % 4 == 0 ? INT64_MAX : 4500 + (T + N) * 2 * K / 6000 + plan_tiles(T, N, padded(K), best);
     if (pad < direct && pad < small && pad < big) return {kPadded, 1};
     return {direct < small && direct < big ? kDirect : small <= big ? kRegsSmall : kRegsBig, 1};
+}
+
+// A call asks twice, for its workspace's size and for the launch: the thread's
+// last plan is kept (making one takes 0.3 to 0.7 us at few tokens).
+inline Q8Plan plan_q8(int64_t T, int64_t N, int64_t K, bool dma) {
+    struct Last {
+        int64_t T, N, K;
+        bool dma;
+        Q8Plan plan;
+    };
+    static thread_local Last last{0, 0, 0, false, {kDirect, 1}};   // T is never 0
+    if (last.T != T || last.N != N || last.K != K || last.dma != dma) last = {T, N, K, dma, make_plan_q8(T, N, K, dma)};
+    return last.plan;
 }
 
 // Workspace of a padded product: x's rows, w's rows, and what their product needs.
