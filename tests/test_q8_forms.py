@@ -141,3 +141,25 @@ def test_forms(size, form, parts, inner):
             ref, size_of = ref + (gm.double() - 1) * base + extra, size_of + ((gm.double() - 1) * base).abs() + extra.abs()
         bad = ~((y.double() - ref).abs() <= 8 * u * size_of + U[dt] * ref.abs() + TINY)
         assert not bool(bad.any()), (size, dt, int(bad.sum()), bad.nonzero()[:4].tolist())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N,K", [(512, 2048), (301, 1003), (5120, 5120)])
+@pytest.mark.parametrize("dt", [torch.float16, torch.float32])
+def test_rows_do_not_depend_on_the_batch(N, K, dt):
+    """Bitwise: the sum is exact and every form ends in the same fp32 steps and
+    one conversion (fp16: none of them may join the last step with it)."""
+    print(f"[q8 forms] batches {N}x{K} {dt}", file=sys.stderr, flush=True)
+    g = torch.Generator(device=DEV).manual_seed(N + K)
+    xq = torch.randint(-127, 128, (700, K), generator=g, device=DEV, dtype=torch.int8)
+    wq = torch.randint(-127, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+    xs, ws = (torch.rand(n, generator=g, device=DEV) * 0.01 + 1e-3 for n in (700, N))
+    gm, bias = 1 + 0.3 * torch.randn(N, generator=g, device=DEV), torch.randn(N, generator=g, device=DEV)
+    lora = torch.randn(700, N, generator=g, device=DEV).to(dt)
+    for adapter in (True, False):
+        y = D.matmul_q8(xq, xs, wq, ws, dt, bias=bias, g=gm if adapter else None, lora_out=lora if adapter else None, s=1.7)
+        for lo, hi in ((0, 1), (3, 7), (10, 40), (100, 170), (200, 500)):
+            part = D.matmul_q8(xq[lo:hi].contiguous(), xs[lo:hi].contiguous(), wq, ws, dt, bias=bias, g=gm if adapter else None,
+                               lora_out=lora[lo:hi].contiguous() if adapter else None, s=1.7)
+            torch.cuda.synchronize()
+            assert torch.equal(part, y[lo:hi]), (adapter, lo, hi)
