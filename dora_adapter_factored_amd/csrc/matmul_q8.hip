@@ -320,9 +320,10 @@ __device__ __forceinline__ i32x4_t* part_at(const TileGrid& g, int part, int tm,
 // Workgroup id -> part of K and tile.  Ids go round the XCDs, so XCD x takes
 // the x-th contiguous part of the order, in which kGroupM token tiles share a
 // channel tile before the next one: the tiles an XCD works on at one time are
-// a block, whose operands' rows meet in its L2.  4 x 8 tiles of 256 x 256: 737
-// us at 4096 x 28672 x 8192, 8 x 4 744, 2 x 16 and 3 x 11 about 760 to 775, 16
-// x 2 772.
+// a block, whose operands' rows meet in its L2.  In turn on one card at 4096 x
+// 28672 x 8192, 256 x 256 tiles: 4 x 8 tiles 736 us, 8 x 4 739; 2 x 16, 3 x 11 and
+// 16 x 2 3 to 5% more.  (The card's power sets the level, 695 to 736 us in
+// several runs; only runs in turn compare.)
 constexpr int kGroupM = 4;
 
 __device__ __forceinline__ void tile_of(int id, const TileGrid& g, int& part, int& m, int& n) {
@@ -525,7 +526,9 @@ __global__ __launch_bounds__(G::NTH, 1) void q8_tiles(MatmulQ8 a, TileGrid grid)
     // back and forth, so that each MFMA has an operand of the one before it: the
     // full chip runs against its power limit (1.85 GHz at 4096 x 28672 x 8192,
     // 4.0 POP/s with operands in registers and nothing else, 4.9 with zeros in
-    // them), and fewer toggled inputs are 1 to 1.7% of the time there
+    // them), and fewer toggled inputs are 0.6 to 1% of the time at sizes that
+    // fill it (735.7 against 742.0 us in turn; 104.1 against 104.8 at 2048 x 8192 x
+    // 8192)
     auto mma = [&](const i32x4_t (&x)[G::MT], const i32x4_t (&w)[G::NC]) __attribute__((always_inline)) {
 #pragma unroll
         for (int m = 0; m < G::MT; ++m)

@@ -23,7 +23,9 @@
 // again from cache.  Measured at 4096 x 8192 in bf16 (a copy of 1 GiB: 5.1
 // TB/s): norm with h and y 49.5 us, 5.4 TB/s; with h and codes 43.3 us, 5.4;
 // rows to 8 bits 18.8 us, 5.4; back 16.8 us, 6.0; backward pass 48.9 us, 5.5,
-// and 57.4 with dw.  A token of 4096: 3.0, 3.7, 2.7, 2.3 and 3.0 us.
+// and 57.4 with dw.  A token of 4096: 3.0, 3.7, 2.7, 2.3 and 3.0 us.  Rows too
+// long for the registers, norm with h and y: 31.5 us at 512 x 33000 in bf16, 4.3
+// TB/s of the bytes that count (30720 in registers: 6.3).
 #include "dora_device.h"
 #include "dora_launch.h"
 
@@ -342,8 +344,12 @@ struct BwdArgs {
 // Rows blockIdx.x, blockIdx.x + gridDim.x, ... of one workgroup, each in
 // registers between its reduction and its store.  Six accesses a thread (eight
 // of fp32), for the longest rows, leave no registers for w and dh: they are
-// loaded where they are used (registers that spill cost more: 60 us instead of 18 at 2048
-// x 5120 when 4 accesses were held to 128).
+// loaded where they are used (with them in registers that spill, 4 accesses held
+// to 128 took 60 us instead of 18 at 2048 x 5120).  Eight of fp32 at 1024 threads
+// still spill 23 registers, 48 where rows are not aligned: 77 us at 512 x 28672,
+// 3.0 TB/s, against 2.6 TB/s of the rows too long for them (512 x 40000, 124 us);
+// six of bf16 do not: 35 us at 512 x 30720, 3.6 TB/s, against 1.8 (512 x 33000, 73
+// us).
 template <typename E, bool AL, int P>
 __global__ __launch_bounds__(P == 4 ? 512 : P == 6 ? 640 : 1024) void rms_bwd_regs(BwdArgs a) {
     constexpr int N = Pack<E>::N;
